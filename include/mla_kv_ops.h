@@ -93,6 +93,47 @@ int mla_kv_compact(const void *src_pool, int64_t src_slots, void *dst_pool, int6
                    const int64_t *dst_base, int32_t num_seqs, int32_t num_nodes, int32_t stride,
                    int32_t max_seq_len, int32_t debug, int32_t *dev_status, mla_stream_t stream);
 
+/*
+ * mla_slot_map_build -- block tables and slot maps from the requests' lengths, on the device:
+ * gives every new token of a step its slot (a prompt's tokens, or a draft tree's nodes) and takes
+ * the pages that this needs from a free list. For sequence b the step's tokens are the positions
+ * [L_b, L_b + n_b), L_b = seq_lens[b], n_b = new_lens[b]; h_b = held_lens[b] >= L_b positions have
+ * a slot already (after mla_tree_accept_commit the rejected nodes' slots behind the prefix are
+ * held), and a page is page_size consecutive slots:
+ *   have_b = ceil(h_b / page_size),  end_b = max(h_b, L_b + n_b),
+ *   take_b = ceil(end_b / page_size) - have_b,  first_b = sum_{c < b} take_c
+ *   block_table[b][have_b + k] = free_pages[free_count - 1 - (first_b + k)]      for k < take_b
+ *   slot_table[b][t] = block_table[b][t / page_size] * page_size + t % page_size  for h_b <= t < end_b
+ *   cu_new[b] = sum_{c < b} n_c  (cu_new[num_seqs] is the sum of all)
+ *   slot_map[cu_new[b] + j] = slot_table[b][L_b + j]  for j < n_b,  and -1 from cu_new[num_seqs] on
+ *   held_out[b] = end_b,  *free_left = *free_count - sum_b take_b
+ * slot_map is what mla_kv4_append takes; its length is fixed on the host, so a captured step
+ * serves any lengths (the padding rows are skipped). The rest of both tables is left as it was.
+ *
+ * All or nothing: when the free pages or the map's capacity do not suffice, no table is changed,
+ * slot_map is all -1, cu_new all 0, held_out = held_lens, *free_left = *free_count
+ * (MLA_CHECK_NO_PAGES under debug). A sequence with L_b < 0, n_b < 0, h_b < L_b or more positions
+ * than its table rows hold is taken as n_b = 0 and end_b = h_b (MLA_CHECK_BAD_LENGTH), and a free_count outside
+ * [0, free_capacity] as too few pages. A page outside [0, num_pages), or a held slot outside
+ * [0, num_pages * page_size), gives the slot -1 to its tokens (MLA_CHECK_BAD_SLOT).
+ *   seq_lens, new_lens  device int32 [num_seqs]; 1 <= num_seqs <= 8192.
+ *   held_lens           device int32 [num_seqs] or NULL (= seq_lens).
+ *   free_pages          device int32 [free_capacity], taken from the end; free_count: device int32.
+ *   block_table         device int32 [num_seqs][block_stride]; NULL only when page_size is 1.
+ *   slot_table          device int32 [num_seqs][slot_stride].
+ *   slot_map            device int32 [map_capacity].
+ *   cu_new              device int32 [num_seqs + 1].
+ *   held_out, free_left device int32 [num_seqs] and [1]; they must not be held_lens (or seq_lens)
+ *                       and free_count themselves: inputs are not written.
+ * page_size >= 1 and num_pages * page_size <= 2^31 - 1; map_capacity <= 2^31 - 1.
+ */
+int mla_slot_map_build(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *held_lens, int32_t num_seqs,
+                       int32_t page_size, int32_t num_pages, const int32_t *free_pages, int32_t free_capacity,
+                       const int32_t *free_count, int32_t *block_table, int32_t block_stride, int32_t *slot_table,
+                       int32_t slot_stride, int32_t *slot_map, int64_t map_capacity, int32_t *cu_new,
+                       int32_t *held_out, int32_t *free_left, int32_t debug, int32_t *dev_status,
+                       mla_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

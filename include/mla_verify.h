@@ -87,7 +87,8 @@ enum mla_device_check {
   MLA_CHECK_BAD_SLOT = 1 << 0,    /* slot_table entry outside [0, num_slots) */
   MLA_CHECK_BAD_PARENT = 1 << 1,  /* tree_parent[i] outside [-1, i) */
   MLA_CHECK_BAD_LENGTH = 1 << 2,  /* seq_lens[b] outside [0, max_seq_len] */
-  MLA_CHECK_TIMEOUT = 1 << 3      /* a bounded wait inside a kernel gave up */
+  MLA_CHECK_TIMEOUT = 1 << 3,     /* a bounded wait inside a kernel gave up */
+  MLA_CHECK_NO_PAGES = 1 << 4     /* mla_slot_map_build: too few free pages, or the map is too short */
 };
 
 /* Shapes of one call. Every field is host-visible, so the launch plan is a pure

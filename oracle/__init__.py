@@ -240,3 +240,108 @@ def kv_compact(src_pool: np.ndarray, slot_table: np.ndarray, seq_lens: np.ndarra
             dst[d] = src_pool[int(slot_table[b, t])]
             table[b, t] = d
     return dst, table
+
+
+# ---------------------------------------------------------------------------------------------
+# The pool held in 4 bits and the slot maps (plain numpy, the definitions written out). A 416-byte row:
+# 512 e2m1 codes (two to a byte, the even dim low), 32 e4m3 scales (one to 16 dims), 64 bf16 RoPE dims.
+
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=np.float64)
+E4M3 = np.array([m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10) for e in range(16) for m in range(8)][:127])
+
+
+def _nearest_code(x: np.ndarray, grid: np.ndarray) -> np.ndarray:
+    """Index of the value of an ascending grid nearest to each x >= 0; the even index at a tie."""
+    i = np.clip(np.searchsorted(grid, x, side="right"), 1, len(grid) - 1)
+    below, above = x - grid[i - 1], grid[i] - x
+    return np.where((above < below) | ((above == below) & (i % 2 == 0)), i, i - 1)
+
+
+def _bf16_values(bits: np.ndarray) -> np.ndarray:
+    return (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def kv4_quantise(bits: np.ndarray) -> np.ndarray:
+    """bf16 rows (uint16 bits [n, 576]) as rows of the 4-bit pool (uint8 [n, 416])."""
+    n = bits.shape[0]
+    x = _bf16_values(np.ascontiguousarray(bits[:, :512])).reshape(n, 32, 16)
+    out = np.zeros((n, 416), dtype=np.uint8)
+    fine = np.isfinite(x).all(axis=2)
+    top = np.where(fine, np.abs(np.where(np.isfinite(x), x, 0)).max(axis=2), 0)
+    scale = _nearest_code(np.minimum(top / 6, 448), E4M3)
+    s = E4M3[scale][:, :, None]
+    y = np.where(fine[:, :, None] & (s > 0), np.where(np.isfinite(x), x, 0) / np.where(s > 0, s, 1), 0)
+    code = _nearest_code(np.minimum(np.abs(y), 6), E2M1) + 8 * (y < 0)
+    code = code.reshape(n, 256, 2).astype(np.uint8)
+    out[:, :256] = code[:, :, 0] | (code[:, :, 1] << 4)
+    out[:, 256:288] = np.where(fine, scale, 127)
+    out[:, 288:] = np.ascontiguousarray(bits[:, 512:]).view(np.uint8).reshape(n, 128)
+    return out
+
+
+def kv4_values(rows: np.ndarray) -> np.ndarray:
+    """Rows of the 4-bit pool (uint8 [n, 416]) as the values they stand for (float64 [n, 576])."""
+    n = rows.shape[0]
+    out = np.empty((n, 576))
+    for k in (0, 1):
+        c = (rows[:, :256] >> (4 * k)) & 15
+        out[:, k:512:2] = np.where(c >= 8, -1.0, 1.0) * E2M1[c & 7]
+    s = rows[:, 256:288]
+    s = np.where((s & 127) == 127, np.nan, np.where(s >= 128, -1.0, 1.0) * E4M3[np.minimum(s & 127, 126)])
+    out[:, :512] *= np.repeat(s, 16, axis=1)
+    out[:, 512:] = _bf16_values(np.ascontiguousarray(rows[:, 288:]).view(np.uint16))
+    return out
+
+
+def kv4_bf16(rows: np.ndarray) -> np.ndarray:
+    """The same values as bf16 bits (uint16 [n, 576]): every one of them is a bf16 number."""
+    v = kv4_values(rows).astype(np.float32)
+    bits = v.view(np.uint32)
+    assert ((bits & 0xFFFF) == 0)[np.isfinite(v)].all()
+    return (bits >> 16).astype(np.uint16)
+
+
+def slot_map_build(seq_lens, new_lens, held_lens, page_size: int, num_pages: int, free_pages, free_count: int,
+                   block_table, slot_table, map_capacity: int):
+    """The definition of mla_slot_map_build, sequence by sequence. Returns (block_table, slot_table, slot_map,
+    cu_new, held_out, free_left, bits) with bits a set of "length", "pages" and "slot" findings; inputs are not modified."""
+    B, p = len(seq_lens), page_size
+    held_lens = seq_lens if held_lens is None else held_lens
+    block, table = None if block_table is None else block_table.copy(), slot_table.copy()
+    slot_map = np.full(map_capacity, -1, dtype=np.int32)
+    found, wish = set(), []
+    for b in range(B):
+        L, n, h = int(seq_lens[b]), int(new_lens[b]), int(held_lens[b])
+        end = max(h, L + n)
+        if L < 0 or n < 0 or h < L or end > table.shape[1] or (block is not None and -(-end // p) > block.shape[1]):
+            found.add("length")
+            n, end = 0, h
+            wish.append((L, n, h, end, 0))
+        else:
+            wish.append((L, n, h, end, -(-end // p) - -(-h // p)))
+    tokens, take = sum(w[1] for w in wish), sum(w[4] for w in wish)
+    if tokens > map_capacity or not 0 <= free_count <= len(free_pages) or take > free_count:
+        found.add("pages")
+        return (block, table, slot_map, np.zeros(B + 1, np.int32), np.array([w[2] for w in wish], np.int32), free_count, found)
+    cu, left = [0], free_count
+    for b, (L, n, h, end, take) in enumerate(wish):
+        have = -(-h // p)
+        pages = [int(free_pages[left - 1 - k]) for k in range(take)]
+        left -= take
+        if block is not None:
+            block[b, have:have + take] = pages
+        for t in range(L, L + n):
+            if t < h:
+                slot = int(table[b, t])
+                bad = not 0 <= slot < num_pages * p
+            else:
+                page = pages[t // p - have] if t // p >= have else int(block[b, t // p])
+                slot, bad = page * p + t % p, not 0 <= page < num_pages
+            if bad:
+                found.add("slot")
+                slot = -1
+            if t >= h:
+                table[b, t] = slot
+            slot_map[cu[-1] + t - L] = slot
+        cu.append(cu[-1] + n)
+    return (block, table, slot_map, np.array(cu, np.int32), np.array([w[3] for w in wish], np.int32), left, found)

@@ -7,10 +7,18 @@ device memory and streams. There is no CPU fallback: if the library is missing
 or no sm_103 device is present, calls raise.
 
     out, lse = verify(q, kv_pool, slot_table, seq_lens, tree_parent, max_seq_len=L)
+
+The same over a pool held in 4 bits (``include/mla_kv4.h``), with the step's slots built on the GPU:
+
+    slot_map, cu_new, held, left = slot_map_build(seq_lens, new_lens, free_pages, free_count, slot_table, ...)
+    kv4_append(pool4, rows, slot_map)
+    out, lse = verify_kv4(q, pool4, slot_table, seq_lens, tree_parent, max_seq_len=L)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -21,8 +29,9 @@ LIB_PATH = os.path.join(_PKG, "libmla_verify.so")
 MLA_OK = 0
 MLA_DTYPE_BF16, MLA_DTYPE_F32, MLA_DTYPE_F16 = 0, 1, 2
 MLA_FLAG_DEBUG_CHECKS, MLA_FLAG_SIMT, MLA_FLAG_PREFIX_STABLE = 1, 2, 4
-CHECK_BAD_SLOT, CHECK_BAD_PARENT, CHECK_BAD_LENGTH, CHECK_TIMEOUT = 1, 2, 4, 8
+CHECK_BAD_SLOT, CHECK_BAD_PARENT, CHECK_BAD_LENGTH, CHECK_TIMEOUT, CHECK_NO_PAGES = 1, 2, 4, 8, 16
 D_LATENT, D_ROPE = 512, 64
+KV4_ROW_BYTES = 416  # a row of the 4-bit pool
 DEFAULT_SCALE = 1.0 / math.sqrt(192.0)
 
 # The kernel a default call runs (the tcgen05 kernel): flags used unless a call overrides them.
@@ -74,10 +83,17 @@ def load_library(path: str = LIB_PATH):
     lib.mla_tree_kv_append.argtypes = [P, i64, P, P, P, i32, i32, i32, i32, i32, P, P]
     lib.mla_tree_accept_commit.argtypes = [P, P, P, P, P, i32, i32, i32, i32, i32, P, P]
     lib.mla_kv_compact.argtypes = [P, i64, P, i64, P, P, P, P, i32, i32, i32, i32, i32, P, P]
+    lib.mla_slot_map_build.argtypes = [P, P, P, i32, i32, i32, P, i32, P, P, i32, P, i32, P, i64, P, P, P, i32, P, P]
+    lib.mla_kv4_append.argtypes = [P, i64, P, i64, P, i64, i32, P, P]
+    lib.mla_kv4_gather.argtypes = [P, i64, P, i64, P, i32, P, P]
+    lib.mla_verify_kv4_plan.argtypes = [ctypes.POINTER(Desc), i32, ctypes.POINTER(Plan)]
+    lib.mla_verify_kv4_workspace_size.argtypes = [ctypes.POINTER(Desc), ctypes.POINTER(ctypes.c_size_t)]
+    lib.mla_verify_attn_kv4.argtypes = [ctypes.POINTER(Desc), P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P]
     for f in ("mla_verify_plan", "mla_verify_workspace_size", "mla_verify_attn", "mla_verify_attn_partials",
               "mla_verify_attn_hybrid", "mla_verify_attn_ragged",
               "mla_verify_combine", "mla_fill_normal_bf16", "mla_tree_kv_append", "mla_tree_accept_commit",
-              "mla_kv_compact"):
+              "mla_kv_compact", "mla_slot_map_build", "mla_kv4_append", "mla_kv4_gather", "mla_verify_kv4_plan",
+              "mla_verify_kv4_workspace_size", "mla_verify_attn_kv4"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -277,6 +293,185 @@ def kv_compact(src_pool, dst_pool, slot_table, seq_lens, dst_base, *, num_nodes:
                                        max_seq_len, int(debug), _ptr_or_none(dev_status), _stream_ptr(stream))
     _check(rc, "mla_kv_compact")
     return dst_pool, new_slot_table
+
+
+def _check_tensor(name: str, t, dtype, shape, device):
+    """A contiguous CUDA tensor of this type, shape (None: any extent) and device, or ValueError."""
+    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}: got {t.dtype} on {t.device}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}: got {tuple(t.shape)}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """(stream, context): the context makes the device and the stream current, so that what a call
+    allocates belongs to the stream that its kernels run on."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+        if torch.cuda.current_device() == device.index:
+            return stream, _HERE
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream, torch.cuda.stream(stream)
+
+
+def slot_map_build(seq_lens, new_lens, free_pages, free_count, slot_table, *, page_size: int, num_pages: int,
+                   map_capacity: Optional[int] = None, held_lens=None, block_table=None, slot_map=None, cu_new=None,
+                   held_out=None, free_left=None, debug: bool = False, dev_status=None, stream=None):
+    """Slots for every new token of a step, with pages from a free list (``include/mla_kv_ops.h``).
+
+    seq_lens, new_lens, held_lens: int32 [B]; free_pages: int32 [any]; free_count: int32 [1]; slot_table: int32
+    [B, stride] and block_table: int32 [B, blocks] are extended in place (block_table may be None when page_size is 1).
+    Returns (slot_map [map_capacity], cu_new [B + 1], held_out [B], free_left [1]); each may be passed in.
+    """
+    import torch
+    dev, B, i32 = seq_lens.device, seq_lens.shape[0], torch.int32
+    if map_capacity is None:
+        if slot_map is None:
+            raise ValueError("map_capacity or slot_map is needed")
+        map_capacity = slot_map.numel()
+    s, here = _on(dev, stream)
+    with here:
+        if slot_map is None:
+            slot_map = torch.empty(map_capacity, dtype=i32, device=dev)
+        if cu_new is None:
+            cu_new = torch.empty(B + 1, dtype=i32, device=dev)
+        if held_out is None:
+            held_out = torch.empty(B, dtype=i32, device=dev)
+        if free_left is None:
+            free_left = torch.empty(1, dtype=i32, device=dev)
+        for name, t, shape in (("seq_lens", seq_lens, (B,)), ("new_lens", new_lens, (B,)), ("held_lens", held_lens, (B,)),
+                               ("free_pages", free_pages, (None,)), ("free_count", free_count, (1,)),
+                               ("slot_table", slot_table, (B, None)), ("block_table", block_table, (B, None)),
+                               ("slot_map", slot_map, (map_capacity,)), ("cu_new", cu_new, (B + 1,)),
+                               ("held_out", held_out, (B,)), ("free_left", free_left, (1,)),
+                               ("dev_status", dev_status, (1,))):
+            if t is not None:
+                _check_tensor(name, t, i32, shape, dev)
+        rc = load_library().mla_slot_map_build(
+            seq_lens.data_ptr(), new_lens.data_ptr(), _ptr_or_none(held_lens), B, page_size, num_pages,
+            free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), _ptr_or_none(block_table),
+            0 if block_table is None else block_table.shape[1], slot_table.data_ptr(), slot_table.shape[1],
+            slot_map.data_ptr(), map_capacity, cu_new.data_ptr(), held_out.data_ptr(), free_left.data_ptr(), int(debug),
+            _ptr_or_none(dev_status), s.cuda_stream)
+    _check(rc, "mla_slot_map_build")
+    return slot_map, cu_new, held_out, free_left
+
+
+def kv4_append(pool, rows, slot_map, *, debug: bool = False, dev_status=None, stream=None):
+    """Quantise bf16 rows [n, 576] (rows may be strided, dims contiguous) into pool[slot_map[i]] of the 4-bit pool
+    uint8 [slots, 416] (``include/mla_kv4.h``); slot -1 skips a row. In place on pool."""
+    import torch
+    dev, n = pool.device, rows.shape[0]
+    _check_tensor("pool", pool, torch.uint8, (None, KV4_ROW_BYTES), dev)
+    _check_tensor("slot_map", slot_map, torch.int32, (n,), dev)
+    if rows.dtype != torch.bfloat16 or rows.device != dev or rows.dim() != 2 or rows.shape[1] != D_LATENT + D_ROPE:
+        raise ValueError(f"rows must be bf16 [n, 576] on {dev}: got {rows.dtype} {tuple(rows.shape)} on {rows.device}")
+    if rows.stride(1) != 1:
+        raise ValueError("the dims of a row must be contiguous")
+    if dev_status is not None:
+        _check_tensor("dev_status", dev_status, torch.int32, (1,), dev)
+    s, here = _on(dev, stream)
+    with here:
+        rc = load_library().mla_kv4_append(pool.data_ptr(), pool.shape[0], rows.data_ptr(),
+                                           rows.stride(0) if n > 1 else D_LATENT + D_ROPE, slot_map.data_ptr(), n,
+                                           int(debug), _ptr_or_none(dev_status), s.cuda_stream)
+    _check(rc, "mla_kv4_append")
+    return pool
+
+
+def kv4_gather(pool, slots, *, out=None, debug: bool = False, dev_status=None, stream=None):
+    """Rows of the 4-bit pool as bf16 [n, 576], exactly; slot -1 gives zeros (``include/mla_kv4.h``)."""
+    import torch
+    dev, n = pool.device, slots.shape[0]
+    _check_tensor("pool", pool, torch.uint8, (None, KV4_ROW_BYTES), dev)
+    _check_tensor("slots", slots, torch.int32, (n,), dev)
+    if dev_status is not None:
+        _check_tensor("dev_status", dev_status, torch.int32, (1,), dev)
+    s, here = _on(dev, stream)
+    with here:
+        if out is None:
+            out = torch.empty((n, D_LATENT + D_ROPE), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_tensor("out", out, torch.bfloat16, (n, D_LATENT + D_ROPE), dev)
+        rc = load_library().mla_kv4_gather(pool.data_ptr(), pool.shape[0], slots.data_ptr(), n, out.data_ptr(),
+                                           int(debug), _ptr_or_none(dev_status), s.cuda_stream)
+    _check(rc, "mla_kv4_gather")
+    return out
+
+
+def kv4_plan(desc: Desc, num_sms: int) -> Plan:
+    p = Plan()
+    _check(load_library().mla_verify_kv4_plan(ctypes.byref(desc), int(num_sms), ctypes.byref(p)),
+           "mla_verify_kv4_plan")
+    return p
+
+
+def kv4_workspace_size(desc: Desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().mla_verify_kv4_workspace_size(ctypes.byref(desc), ctypes.byref(n)),
+           "mla_verify_kv4_workspace_size")
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=256)
+def _kv4_desc(device_index, *shape):
+    """(desc, workspace bytes) of a call's shapes: a pure function of them and of the device's SM count."""
+    B, T, H, slots, stride, max_seq_len, scale, out_dtype, flags, splits, hint = shape
+    desc = make_desc(B, T, H, slots, stride, max_seq_len, softmax_scale=scale, out_dtype=out_dtype, flags=flags,
+                     num_splits=splits, total_tokens_hint=hint)
+    return desc, kv4_workspace_size(desc)
+
+
+def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, softmax_scale: float = DEFAULT_SCALE,
+               out_dtype: int = MLA_DTYPE_BF16, flags: Optional[int] = None, num_splits: int = 0,
+               total_tokens_hint: int = 0, tree_sizes=None, out=None, lse=None, workspace=None, dev_status=None,
+               stream=None):
+    """Tree-verify attention over the 4-bit pool uint8 [slots, 416] (``include/mla_kv4.h``); otherwise as verify().
+
+    q: bf16 [B*T, H, 576]; slot_table: int32 [B, stride]; seq_lens: int32 [B]; tree_parent: int32 [B, T];
+    tree_sizes: int32 [B] or None. Returns (out [B*T, H, 512], lse [B*T, H]).
+    """
+    import torch
+    dev, i32 = q.device, torch.int32
+    B, T = tree_parent.shape
+    H = q.shape[1]
+    out_type = torch.bfloat16 if out_dtype == MLA_DTYPE_BF16 else torch.float32
+    _check_tensor("q", q, torch.bfloat16, (B * T, H, D_LATENT + D_ROPE), dev)
+    _check_tensor("pool", pool, torch.uint8, (None, KV4_ROW_BYTES), dev)
+    _check_tensor("slot_table", slot_table, i32, (B, None), dev)
+    _check_tensor("seq_lens", seq_lens, i32, (B,), dev)
+    _check_tensor("tree_parent", tree_parent, i32, (B, T), dev)
+    if tree_sizes is not None:
+        _check_tensor("tree_sizes", tree_sizes, i32, (B,), dev)
+    if dev_status is not None:
+        _check_tensor("dev_status", dev_status, i32, (1,), dev)
+    s, here = _on(dev, stream)
+    with here:
+        desc, need = _kv4_desc(dev.index, B, T, H, pool.shape[0], slot_table.shape[1], max_seq_len, softmax_scale,
+                               out_dtype, DEFAULT_FLAGS if flags is None else flags, num_splits, total_tokens_hint)
+        if out is None:
+            out = torch.empty((B * T, H, D_LATENT), device=dev, dtype=out_type)
+        else:
+            _check_tensor("out", out, out_type, (B * T, H, D_LATENT), dev)
+        if lse is None:
+            lse = torch.empty((B * T, H), device=dev, dtype=torch.float32)
+        else:
+            _check_tensor("lse", lse, torch.float32, (B * T, H), dev)
+        if workspace is None:
+            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        else:
+            _check_tensor("workspace", workspace, torch.uint8, (None,), dev)
+        rc = load_library().mla_verify_attn_kv4(
+            ctypes.byref(desc), q.data_ptr(), pool.data_ptr(), slot_table.data_ptr(), seq_lens.data_ptr(),
+            _ptr_or_none(tree_sizes), tree_parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _ptr_or_none(dev_status), s.cuda_stream)
+    _check(rc, "mla_verify_attn_kv4")
+    return out, lse
 
 
 def _ptr_or_none(t):

@@ -17,6 +17,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+}  // namespace
+
 int check_desc(const mla_verify_desc* d) {
   if (!d) return MLA_ERR_INVALID_ARGUMENT;
   if (d->d_latent != kDLatent || d->d_rope != kDRope) return MLA_ERR_UNSUPPORTED;
@@ -33,8 +35,6 @@ int check_desc(const mla_verify_desc* d) {
   if ((int64_t)d->num_seqs * d->slot_table_stride > (1ll << 40)) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
-
-}  // namespace
 }  // namespace mla
 
 using namespace mla;
@@ -100,7 +100,7 @@ extern "C" int mla_verify_plan(const mla_verify_desc* d, int32_t num_sms, mla_ve
   return MLA_OK;
 }
 
-namespace {
+namespace mla {
 int current_sms(int32_t* sms) {
   int dev = 0, n = 0, major = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_NO_DEVICE;
@@ -110,7 +110,7 @@ int current_sms(int32_t* sms) {
   *sms = n;
   return MLA_OK;
 }
-}  // namespace
+}  // namespace mla
 
 extern "C" int mla_verify_workspace_size(const mla_verify_desc* d, size_t* bytes) {
   if (!bytes) return MLA_ERR_INVALID_ARGUMENT;
@@ -197,8 +197,9 @@ int run_splits(const mla_verify_desc* d, const void* q, const void* kv_pool, con
   *args_out = a;
   return MLA_OK;
 }
+}  // namespace
 
-// With debug checks: wait for the stream and turn a non-zero device status into an error.
+namespace mla {
 int finish_debug(const mla_verify_desc* d, int32_t* dev_status, cudaStream_t s) {
   if (!(d->flags & MLA_FLAG_DEBUG_CHECKS)) return MLA_OK;
   int32_t h = 0;
@@ -206,7 +207,7 @@ int finish_debug(const mla_verify_desc* d, int32_t* dev_status, cudaStream_t s) 
   if (cudaStreamSynchronize(s) != cudaSuccess) return MLA_ERR_CUDA;
   return h != 0 ? MLA_ERR_DEVICE_CHECK : MLA_OK;
 }
-}  // namespace
+}  // namespace mla
 
 extern "C" int mla_verify_attn(const mla_verify_desc* d, const void* q, const void* kv_pool,
                                const int32_t* slot_table, const int32_t* seq_lens, const int32_t* tree_parent,

@@ -1,0 +1,121 @@
+// C ABI of tree-verify attention over the 4-bit pool: planner and dispatch (include/mla_kv4.h).
+#include <string.h>
+
+#include "kv4.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kSimtRowsPerTile = 8;  // one warp per row, 8 warps per CTA
+constexpr int kMaxSplits = 65535;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int64_t part_o_bytes(const mla_verify_plan_t& p, int64_t rows) {
+  return cdiv((int64_t)p.num_splits * rows * kDLatent * 2, 256) * 256;
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, mla_verify_plan_t* plan) {
+  int rc = check_desc(d);
+  if (rc) return rc;
+  if (!plan || num_sms < 1) return MLA_ERR_INVALID_ARGUMENT;
+  mla_verify_plan_t p;
+  memset(&p, 0, sizeof p);
+  p.kernel = 1;
+  p.rows_per_tile = kSimtRowsPerTile;
+  const int64_t R = (int64_t)d->num_nodes * d->num_heads;
+  p.row_tiles = (int32_t)cdiv(R, p.rows_per_tile);
+  const int64_t max_n = (int64_t)d->max_seq_len + d->num_nodes;
+  const int64_t max_tiles = cdiv(max_n, kTileTokens);
+  const int64_t slots = (int64_t)num_sms * 8;
+  int64_t tiles = d->num_splits > 0 ? cdiv(max_tiles, d->num_splits)
+                                    : cdiv(max_tiles * d->num_seqs * p.row_tiles, slots);
+  tiles = tiles < 1 ? 1 : tiles > max_tiles ? max_tiles : tiles;
+  if (cdiv(max_tiles, tiles) > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits);
+  p.chunk_tokens = (int32_t)(tiles * kTileTokens);
+  p.num_splits = (int32_t)cdiv(max_n, p.chunk_tokens);
+  const int64_t units = (int64_t)d->num_seqs * p.row_tiles * p.num_splits;
+  if (units > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
+  p.ctas = (int32_t)units;
+  const int64_t rows = (int64_t)d->num_seqs * R;
+  p.workspace_bytes = part_o_bytes(p, rows) + cdiv((int64_t)p.num_splits * rows * 4, 256) * 256;
+  *plan = p;
+  return MLA_OK;
+}
+
+extern "C" int mla_verify_kv4_workspace_size(const mla_verify_desc* d, size_t* bytes) {
+  if (!bytes) return MLA_ERR_INVALID_ARGUMENT;
+  int rc = check_desc(d);
+  if (rc) return rc;
+  int32_t sms = 0;
+  rc = current_sms(&sms);
+  if (rc) return rc;
+  mla_verify_plan_t p;
+  rc = mla_verify_kv4_plan(d, sms, &p);
+  if (rc) return rc;
+  *bytes = (size_t)p.workspace_bytes;
+  return MLA_OK;
+}
+
+extern "C" int mla_verify_attn_kv4(const mla_verify_desc* d, const void* q, const void* pool,
+                                   const int32_t* slot_table, const int32_t* seq_lens, const int32_t* tree_sizes,
+                                   const int32_t* tree_parent, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_status, mla_stream_t stream) {
+  int rc = check_desc(d);
+  if (rc) return rc;
+  if (!q || !pool || !slot_table || !seq_lens || !tree_parent || !out || !lse || !workspace)
+    return MLA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256) ||
+      !aligned(slot_table, 4) || !aligned(seq_lens, 4) || !aligned(tree_sizes, 4) || !aligned(tree_parent, 4))
+    return MLA_ERR_INVALID_ARGUMENT;
+  const bool debug = (d->flags & MLA_FLAG_DEBUG_CHECKS) != 0;
+  if (debug && !dev_status) return MLA_ERR_INVALID_ARGUMENT;
+  int32_t sms = 0;
+  rc = current_sms(&sms);
+  if (rc) return rc;
+  mla_verify_plan_t p;
+  rc = mla_verify_kv4_plan(d, sms, &p);
+  if (rc) return rc;
+  if (workspace_bytes < (size_t)p.workspace_bytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+
+  VerifyArgs a;
+  memset(&a, 0, sizeof a);
+  a.rows = (int64_t)d->num_seqs * d->num_nodes * d->num_heads;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv = static_cast<const __nv_bfloat16*>(pool);
+  a.slot_table = slot_table;
+  a.tree_sizes = tree_sizes;
+  a.seq_lens = seq_lens;
+  a.tree_parent = tree_parent;
+  a.part_o = static_cast<__half*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_o_bytes(p, a.rows));
+  a.dev_status = dev_status;
+  a.num_slots = d->num_slots;
+  a.B = d->num_seqs;
+  a.T = d->num_nodes;
+  a.H = d->num_heads;
+  a.stride = d->slot_table_stride;
+  a.max_seq_len = d->max_seq_len;
+  a.chunk = p.chunk_tokens;
+  a.splits = p.num_splits;
+  a.row_tiles = p.row_tiles;
+  a.rows_per_tile = p.rows_per_tile;
+  a.debug = debug ? 1 : 0;
+  a.scale = d->softmax_scale;
+  a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_verify_kv4_simt(a, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_combine(p.num_splits, a.rows, kDLatent, a.part_o, MLA_DTYPE_F16, a.part_lse, out, lse, d->out_dtype,
+                     /*dependent=*/true, s) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return finish_debug(d, dev_status, s);
+}

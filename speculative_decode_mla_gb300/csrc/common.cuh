@@ -21,7 +21,7 @@ constexpr int kLptMaxSeqs = 64;          // longest-first unit order: up to two 
 // Everything a kernel needs, by value (a kernel parameter).
 struct VerifyArgs {
   const __nv_bfloat16* q;
-  const __nv_bfloat16* kv;
+  const __nv_bfloat16* kv;      // bf16 rows; for the kv4 kernels the bytes of the 4-bit pool
   const int32_t* slot_table;    // [B][stride]; unused when hybrid
   const int64_t* prefix_base;   // hybrid addressing: prefix position t of sequence b is slot prefix_base[b] + t
   const int32_t* tree_slots;    // hybrid addressing: tree node j of sequence b is slot tree_slots[b*T + j]
@@ -46,6 +46,7 @@ struct VerifyArgs {
 // Host-side launchers (each returns a cudaError_t from the launch).
 cudaError_t launch_verify_simt(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_verify_tc(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_verify_kv4_simt(const VerifyArgs& a, cudaStream_t stream);  // kv: the 4-bit pool
 // part_dtype: MLA_DTYPE_F32 or MLA_DTYPE_F16. With `dependent`, the launch may start while the
 // preceding kernel on the stream finishes (programmatic dependent launch); the kernel waits
 // for that kernel's results before reading the partials.
@@ -53,6 +54,11 @@ cudaError_t launch_combine(int32_t splits, int64_t rows, int32_t d_v, const void
                            const float* part_lse, void* out, float* lse, int32_t out_dtype, bool dependent,
                            cudaStream_t stream);
 int tc_kernel_supported();
+// Host-side checks shared by the verify entry points: an MLA_* status.
+int check_desc(const mla_verify_desc* d);
+int current_sms(int32_t* sms);
+// With debug checks: wait for the stream and turn a non-zero device status into an error.
+int finish_debug(const mla_verify_desc* d, int32_t* dev_status, cudaStream_t s);
 // cuTensorMapEncodeTiled, looked up once through the runtime's driver entry point (no link to
 // libcuda); nullptr when the driver does not provide it.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
