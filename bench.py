@@ -133,7 +133,7 @@ class ClockSampler:
 
 # the files the tcgen05 attention kernel is built from (with the headers): the ncu traffic
 # record below is only used while they are unchanged
-TC_SOURCES = ["verify_tc.cu", "common.cuh"]
+TC_SOURCES = ["verify_tc.cu", "tc.cuh", "common.cuh"]
 
 
 def traffic_record(fingerprint):
