@@ -6,8 +6,10 @@
 namespace mla {
 namespace {
 
+constexpr int kTcRowsPerTile = 128;  // query rows of a pair of CTAs
 constexpr int kSimtRowsPerTile = 8;  // one warp per row, 8 warps per CTA
 constexpr int kMaxSplits = 65535;
+constexpr int kUnitTiles = 4;        // a unit's fixed cost in tiles of 128 positions
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -28,22 +30,48 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   if (!plan || num_sms < 1) return MLA_ERR_INVALID_ARGUMENT;
   mla_verify_plan_t p;
   memset(&p, 0, sizeof p);
-  p.kernel = 1;
-  p.rows_per_tile = kSimtRowsPerTile;
+  const bool simt = (d->flags & MLA_FLAG_SIMT) != 0;
+  p.kernel = simt ? 1 : 0;
+  p.rows_per_tile = simt ? kSimtRowsPerTile : kTcRowsPerTile;
   const int64_t R = (int64_t)d->num_nodes * d->num_heads;
   p.row_tiles = (int32_t)cdiv(R, p.rows_per_tile);
+  const int64_t tile = simt ? kTileTokens : kKv4TileTokens;
   const int64_t max_n = (int64_t)d->max_seq_len + d->num_nodes;
-  const int64_t max_tiles = cdiv(max_n, kTileTokens);
-  const int64_t slots = (int64_t)num_sms * 8;
-  int64_t tiles = d->num_splits > 0 ? cdiv(max_tiles, d->num_splits)
-                                    : cdiv(max_tiles * d->num_seqs * p.row_tiles, slots);
+  const int64_t max_tiles = cdiv(max_n, tile);
+  const int64_t uniform = (int64_t)d->num_seqs * max_n;
+  const int64_t total = d->total_tokens_hint > 0 && d->total_tokens_hint < uniform ? d->total_tokens_hint : uniform;
+  // Work units are (sequence, row tile, chunk): one pair of SMs each, or small CTAs, several per SM.
+  const int64_t slots = simt ? (int64_t)num_sms * 8 : (num_sms / 2 > 0 ? num_sms / 2 : 1);
+  int64_t tiles = 1;
+  if (d->num_splits > 0) {
+    tiles = cdiv(max_tiles, d->num_splits);
+  } else if (simt || (total < uniform && d->num_seqs <= kLptMaxSeqs)) {
+    // a batch of different lengths, longest units first: the slots' even share of all tiles
+    tiles = cdiv(cdiv(total, tile) * p.row_tiles, slots);
+  } else {
+    // The chunk that minimises the estimated makespan: waves of units x (its tiles + a fixed cost of
+    // kUnitTiles for the set-up, the pipeline's fill and the write-back), plus the combine's reading.
+    double best = 1e300;
+    for (int64_t ct = 1; ct <= max_tiles; ++ct) {
+      const int64_t splits = cdiv(max_tiles, ct);
+      if (splits > kMaxSplits) continue;
+      const int64_t units = total < uniform ? p.row_tiles * (cdiv(total, ct * tile) + d->num_seqs / 2)
+                                            : (int64_t)d->num_seqs * p.row_tiles * splits;
+      const double cost = (double)cdiv(units, slots) * (double)(ct + kUnitTiles) +
+                          0.25 * (double)splits * p.row_tiles * d->num_seqs / slots;
+      if (cost < best - 1e-9) {
+        best = cost;
+        tiles = ct;
+      }
+    }
+  }
   tiles = tiles < 1 ? 1 : tiles > max_tiles ? max_tiles : tiles;
   if (cdiv(max_tiles, tiles) > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits);
-  p.chunk_tokens = (int32_t)(tiles * kTileTokens);
+  p.chunk_tokens = (int32_t)(tiles * tile);
   p.num_splits = (int32_t)cdiv(max_n, p.chunk_tokens);
   const int64_t units = (int64_t)d->num_seqs * p.row_tiles * p.num_splits;
-  if (units > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
-  p.ctas = (int32_t)units;
+  if (units > 0x3fffffff) return MLA_ERR_UNSUPPORTED;
+  p.ctas = (int32_t)(simt ? units : 2 * units);
   const int64_t rows = (int64_t)d->num_seqs * R;
   p.workspace_bytes = part_o_bytes(p, rows) + cdiv((int64_t)p.num_splits * rows * 4, 256) * 256;
   *plan = p;
@@ -107,13 +135,14 @@ extern "C" int mla_verify_attn_kv4(const mla_verify_desc* d, const void* q, cons
   a.splits = p.num_splits;
   a.row_tiles = p.row_tiles;
   a.rows_per_tile = p.rows_per_tile;
+  a.lpt = (p.kernel == 0 && d->num_seqs >= 2 && d->num_seqs <= kLptMaxSeqs) ? 1 : 0;
   a.debug = debug ? 1 : 0;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
-  if (launch_verify_kv4_simt(a, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if ((p.kernel == 1 ? launch_verify_kv4_simt(a, s) : launch_verify_kv4_tc(a, s)) != cudaSuccess) return MLA_ERR_CUDA;
   if (launch_combine(p.num_splits, a.rows, kDLatent, a.part_o, MLA_DTYPE_F16, a.part_lse, out, lse, d->out_dtype,
                      /*dependent=*/true, s) != cudaSuccess)
     return MLA_ERR_CUDA;

@@ -13,6 +13,8 @@ constexpr int kKv4Rope = kKv4Codes + kKv4Scales;           // the RoPE dims star
 constexpr int kKv4Row = kKv4Rope + 2 * kDRope;             // 416 bytes
 static_assert(kKv4Row == MLA_KV4_ROW_BYTES && kKv4Row % 16 == 0, "row format");
 
+constexpr int kKv4TileTokens = 128;                        // positions per tile of the tcgen05 kernel
+
 // The two values of a code byte (dim 2i low, dim 2i+1 high) as packed fp16, exact.
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
   uint32_t h;
