@@ -15,22 +15,22 @@
 // scaled by a power of two so that its largest magnitude lies in [2^14, 2^15): its bf16 values are then exact
 // in fp16 down to 2^-29 of the largest, and the scale is taken out of the scores.
 //
-//   warps 0-7    gather and dequantise: four threads a key. Codes go from global memory through registers
+//   warps 0-15   gather and dequantise: eight threads a key. Codes go from global memory through registers
 //                (loads of a tile are out before the one before it is used), cvt e2m1x2 -> f16x2, times the block's
-//                scale, to 128B-swizzled shared memory: K into a ring of 16 KB sub-stages (128 dims of 64
+//                scale, to 128B-swizzled shared memory: K into a ring of 32 KB half tiles (256 dims of 64
 //                keys), then, one tile later, V. A value's codes are read once for both.
-//   warps 8-11   softmax, two threads a row (64 keys each): S from TMEM, ancestor bitmask on tree positions, row
+//   warps 16-19  softmax, two threads a row (64 keys each): S from TMEM, ancestor bitmask on tree positions, row
 //                maximum over the two threads through shared memory, exp2, P (fp16) to shared memory; O is
 //                rescaled only when the running maximum grows by more than 2^8. Epilogue: O / l to the workspace.
-//   warp 12, 13  one thread each: CTA 0 issues S and PV for the pair; CTA 1 tells CTA 0 what is ready
+//   warp 20, 21  one thread each: CTA 0 issues S and PV for the pair; CTA 1 tells CTA 0 what is ready
 //                (local barriers, then one remote arrive each: a cluster-scope release is slow, so the
 //                working warps stay off it).
 //
 // P is kept as 2^(s - m + 7): under the lazy maximum it is at most 2^15, and weights down to 2^-32 of a
 // row's largest still count in fp16. l is the fp32 sum of the unrounded weights.
 //
-// TMEM (512 columns): O [0, 256), S [256, 320), Q's dims 0..383 [320, 512) (both lane halves hold the
-// CTA's 64 rows); Q's dims 384..511 and RoPE dims are in shared memory.
+// TMEM (512 columns): O [0, 256), two S buffers [256, 384), Q's dims 0..255 [384, 512) (both lane halves hold the
+// CTA's 64 rows); Q's dims 256..511 and RoPE dims are in shared memory.
 //
 // Positions past a chunk's end read slot 0's row and are masked; values whose scale is NaN are 0
 // in V (their K is NaN, so every row that sees the key is NaN through its weight, and no other).
@@ -49,39 +49,40 @@ constexpr int kCtaRows = 64;   // of them on each CTA
 constexpr int kKeys = kKv4TileTokens;  // 128 positions per tile (S MMA N)
 constexpr int kOwn = 64;       // of them supplied by each CTA
 constexpr int kBlock = kOwn * 128;       // 64 keys (or rows) x 64 dims, 128B swizzle
-constexpr int kKSlots = 6;               // K ring: sub-stages of 128 dims (two blocks) of the own 64 keys
-constexpr int kKSlotBytes = 2 * kBlock;
+constexpr int kKSlots = 3;               // K ring: half tiles, 256 dims (four blocks) of the own 64 keys
+constexpr int kKSlotBytes = 4 * kBlock;
 constexpr int kVBlock = kKeys * 128;     // 128 keys x 64 dims
 constexpr int kVHalfBytes = 2 * kVBlock; // 128 value dims
 constexpr int kSmemK = 0;
-constexpr int kSmemR = kSmemK + kKSlots * kKSlotBytes;  // RoPE dims of the own keys, two tiles
-constexpr int kSmemV = kSmemR + 2 * kBlock;
+constexpr int kSmemR = kSmemK + kKSlots * kKSlotBytes;  // RoPE dims of the own keys
+constexpr int kSmemV = kSmemR + kBlock;
 constexpr int kSmemP = kSmemV + 2 * kVHalfBytes;        // two blocks of 64 rows x 64 keys
-constexpr int kSmemQ = kSmemP + 2 * kBlock;             // dims 384..447, 448..511, RoPE
-constexpr int kSmemX = kSmemQ + 3 * kBlock;             // exchange between the two threads of a row: [2][128] floats
+constexpr int kSmemQ = kSmemP + 2 * kBlock;             // dims 256..511 (four blocks), RoPE
+constexpr int kSmemX = kSmemQ + 5 * kBlock;             // exchange between the two threads of a row: [2][128] floats
 constexpr int kSmemBar = kSmemX + 1024;
 constexpr int kSmemBytes = kSmemBar + 512 + 1024;       // barriers, TMEM slot, tree parents + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory");
 // Q's rows pass through V and P on their way in (64 rows x 1152 bytes)
 static_assert(2 * kVHalfBytes + 2 * kBlock >= kCtaRows * kDK * 2, "Q staging");
 
-constexpr int kDequantWarps = 8;
-constexpr int kSWarp = 12, kPVWarp = 13;  // 8..11: softmax, TMEM lane quarters 0..3; 14 and 15 only fill the warpgroup
-constexpr int kThreads = 16 * 32;
-// Registers a thread: 128 at launch (4 warpgroups x 128 x 128 = 65,536); the issuers' warpgroup hands 72 of its
-// own to the softmax warpgroup (128 + 128 + 200 + 56 = 4 x 128).
-constexpr int kSoftmaxRegs = 200, kIssuerRegs = 56;
+constexpr int kDequantWarps = 16;
+constexpr int kSWarp = 20, kPVWarp = 21;  // 16..19: softmax, TMEM lane quarters 0..3; 22 and 23 only fill the warpgroup
+constexpr int kThreads = 24 * 32;
+// Registers a thread: 80 at launch (768 threads); the other warpgroups hand some of theirs to the softmax
+// warpgroup: 4 x 64 + 168 + 56 = 6 x 80.
+constexpr int kDequantRegs = 64, kSoftmaxRegs = 168, kIssuerRegs = 56;
 constexpr int kParentThread0 = kSWarp * 32;  // 64 threads read the tree parents
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
-constexpr int kQTmemDims = 384;
+constexpr uint32_t kColO = 0, kColS = 256 /* two buffers of 64 */, kColQ = 384;
+constexpr int kQTmemDims = 256;
+constexpr int kQChunks = kDK * 2 / 16;  // 72 16-byte chunks of a query row
 constexpr float kPBias = 7.f;
 
 constexpr int kBarKFull = 0, kBarKEmpty = kKSlots, kBarVFull = 2 * kKSlots /*2*/, kBarVEmpty = kBarVFull + 2 /*2*/,
-              kBarSFull = kBarVEmpty + 2, kBarSEmpty = kBarSFull + 1, kBarPFull = kBarSFull + 2,
-              kBarPEmpty = kBarSFull + 3, kBarQFull = kBarSFull + 4, kBarDrainS = kBarSFull + 5,
-              kBarDrainP = kBarSFull + 6, kNumBars = kBarSFull + 7;
+              kBarSFull = kBarVEmpty + 2 /*2*/, kBarSEmpty = kBarSFull + 2 /*2*/, kBarPFull = kBarSEmpty + 2,
+              kBarPEmpty = kBarPFull + 1, kBarQFull = kBarPFull + 2, kBarDrainS = kBarPFull + 3,
+              kBarDrainP = kBarPFull + 4, kNumBars = kBarPFull + 5;
 static_assert(8 * kNumBars + 8 + 4 * kMaxNodes <= 512, "barrier area");
 
 // Instruction descriptor for kind::f16 with fp32 D: A and B both fp16 or both bf16.
@@ -118,17 +119,27 @@ __device__ __forceinline__ void commit_own(uint32_t bar) {
       "h"((uint16_t)1)
       : "memory");
 }
-__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// v = *p where `on`, else v = other (16 bytes, and 2 bytes widened). The registers are read and written by one
+// predicated instruction each: a load that reaches the next iteration through a branch gets a copy at the
+// branch's end, and the copy waits for the load (about 1700 cycles a tile).
+__device__ __forceinline__ void ld16_or(uint4& v, const uint8_t* p, bool on, uint4 other) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n"
+      "@!p mov.b32 %0, %6;\n@!p mov.b32 %1, %7;\n@!p mov.b32 %2, %8;\n@!p mov.b32 %3, %9;\n"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((int)on), "r"(other.x), "r"(other.y), "r"(other.z), "r"(other.w));
 }
-__device__ __forceinline__ uint32_t ld2(const uint8_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-  return v;
+__device__ __forceinline__ void ld2_or(uint32_t& v, const uint8_t* p, bool on, uint32_t other) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@!p mov.b32 %0, %3;\n@p ld.global.nc.u16 %0, [%1];\n}"
+               : "+r"(v)
+               : "l"(p), "r"((int)on), "r"(other));
+}
+// Arrives on a barrier of the partner CTA. What this thread has acquired from its own CTA's barriers is shared
+// memory, so the release is restricted to that; a full cluster-scope release took about 1500 cycles.
+__device__ __forceinline__ void arrive_partner(uint32_t cluster_bar) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // Two threads a row: warps w and w + 2 of the softmax warps.
 __device__ __forceinline__ void row_pair_sync(int softmax_warp) {
@@ -136,10 +147,11 @@ __device__ __forceinline__ void row_pair_sync(int softmax_warp) {
   else asm volatile("bar.sync 1, 64;" ::: "memory");
 }
 
-// 32 values (a 16-byte piece of a row's codes, its two scales as fp16) into four 16-byte chunks, c0 .. c0 + 3
-// of the 128-byte row at `row_addr` (128B swizzle: chunk c lies at c ^ (row & 7)).
-__device__ __forceinline__ void dequant_piece(uint4 code, uint32_t scales, uint32_t row_addr, uint32_t c0, uint32_t r7) {
-  const uint32_t s0 = __byte_perm(scales, 0, 0x1010), s1 = __byte_perm(scales, 0, 0x3232);
+// 32 values (a 16-byte piece of a row's codes, its two scales as fp16; word j = 8 values) into four 16-byte chunks of
+// a 128-byte row: word j at `at` ^ 16 j, where `at` is the place of word 0 (128B swizzle: chunk c lies at c ^ (row & 7)).
+// `swap`: the words come in the order 2, 3, 0, 1, so the scales change places.
+__device__ __forceinline__ void dequant_piece(uint4 code, uint32_t scales, bool swap, uint32_t at) {
+  const uint32_t s0 = __byte_perm(scales, 0, swap ? 0x3232 : 0x1010), s1 = __byte_perm(scales, 0, swap ? 0x1010 : 0x3232);
   const uint32_t w[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -155,7 +167,7 @@ __device__ __forceinline__ void dequant_piece(uint4 code, uint32_t scales, uint3
       const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), *reinterpret_cast<const __half2*>(&s));
       h[k] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    st_shared_v4(row_addr + (((c0 + (uint32_t)j) ^ r7) << 4), h);
+    st_shared_v4(at ^ (uint32_t)(16 * j), h);
   }
 }
 // Scales that are NaN become 0 (for V; see the top).
@@ -216,8 +228,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
       mbar_init(bar(kBarVFull + i), kDequantWarps + relay);
       mbar_init(bar(kBarVEmpty + i), 1);
     }
-    mbar_init(bar(kBarSFull), 1);
-    mbar_init(bar(kBarSEmpty), 4 + relay);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarSFull + i), 1);
+      mbar_init(bar(kBarSEmpty + i), 4 + relay);
+    }
     mbar_init(bar(kBarPFull), 4 + relay);
     mbar_init(bar(kBarPEmpty), 1);
     mbar_init(bar(kBarQFull), 4 + relay);
@@ -244,52 +258,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
 
-  // ------------------------------------------------------------------ what the gather needs first
-  // Thread (key, qd): lane = 8 qd + key % 8, warp = key / 8; pieces 4i + qd (32 dims each) of a row, i < 4.
-  const int key = warp * 8 + (lane & 7), qd = lane >> 3;
-  const uint8_t* pool = reinterpret_cast<const uint8_t*>(a.kv);
-  const int32_t* tab = a.slot_table + (int64_t)b * a.stride;
-  auto row_at = [&](int t, uint32_t of_rank) -> const uint8_t* {  // the row of position `key` of a CTA's share of tile t
-    const int64_t pos = t0 + (int64_t)t * kKeys + (int)of_rank * kOwn + key;
-    int64_t slot = 0;
-    if (pos < t1) {
-      slot = tab[pos];
-      if (slot < 0 || slot >= a.num_slots) {
-        report(a.dev_status, a.debug, MLA_CHECK_BAD_SLOT);
-        slot = slot < 0 ? 0 : a.num_slots - 1;
+  // Q: the CTA's 64 rows into staging rows (V's and P's place), 16-byte chunk c of row r at c ^ (r & 7); rows of
+  // padding nodes and past the sequence are zeros.
+  {
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + ((int64_t)b * R + row0) * kDK);
+    const int rows = max(0, min(kCtaRows, min(R, Tb * a.H) - row0));
+    for (int i = threadIdx.x; i < kCtaRows * kQChunks; i += kThreads) {
+      const int r = i / kQChunks, c = i % kQChunks;
+      const uint32_t dst = base + kSmemV + r * (kDK * 2) + ((uint32_t)(c ^ (r & 7)) << 4);
+      if (r < rows) {
+        cp_async16(dst, q + (int64_t)i * 16);
+      } else {
+        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+        st_shared_v4(dst, zero);
       }
     }
-    return pool + slot * kKv4Row;
-  };
-  uint4 kc[4], kr[2], pc[2];
-  uint32_t ks[4], ps[2];
-  auto load_own = [&](const uint8_t* row) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kc[i] = ld16(row + 16 * (4 * i + qd));
-      ks[i] = ld2(row + kKv4Codes + 2 * (4 * i + qd));
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) kr[i] = ld16(row + kKv4Rope + 32 * qd + 16 * i);
-  };
-  auto load_peer = [&](const uint8_t* row) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int piece = 4 * ((int)rank + 2 * j) + qd;
-      pc[j] = ld16(row + 16 * piece);
-      ps[j] = ld2(row + kKv4Codes + 2 * piece);
-    }
-  };
-  const uint8_t *own_next = pool, *peer_next = pool;
-  if (warp < kDequantWarps) {
-    const uint8_t* own = row_at(0, rank);
-    const uint8_t* peer = row_at(0, rank ^ 1u);
-    load_own(own);
-    load_peer(peer);
-    own_next = row_at(1, rank);
-    peer_next = row_at(1, rank ^ 1u);
   }
 
+  // ------------------------------------------------------------------ what the gather needs first
+  // Eight threads a key: thread (key, pc) with key = 4 warp + lane / 8, pc = lane % 8. For K it takes the pieces (32 dims)
+  // 8i + pc of its own key's row, i < 2. For V (the dims of pieces 8j + 4 rank + pc % 4) the threads with pc / 4 == rank use
+  // the same codes again, the others take the partner's key. A load of a warp is then four runs of 128 bytes.
+  const int key = warp * 4 + (lane >> 3), pc = lane & 7;
+  const bool v_own = (pc >> 2) == (int)rank;
+  const uint8_t* pool = reinterpret_cast<const uint8_t*>(a.kv);
+  const int32_t* tab = a.slot_table + (int64_t)b * a.stride;
+  // The slot of position `key` of a CTA's share of tile t (positions past the end: 0), and its row. The slot is
+  // loaded two tiles before its row is, and looked at only then.
+  auto slot_at = [&](int t, uint32_t of_rank) -> int32_t {
+    const int64_t pos = t0 + (int64_t)t * kKeys + (int)of_rank * kOwn + key;
+    return pos < t1 ? tab[pos] : 0;
+  };
+  auto row_of = [&](int32_t slot) -> const uint8_t* {
+    if (slot < 0 || slot >= a.num_slots) {
+      report(a.dev_status, a.debug, MLA_CHECK_BAD_SLOT);
+      slot = slot < 0 ? 0 : (int32_t)(a.num_slots - 1);
+    }
+    return pool + (int64_t)slot * kKv4Row;
+  };
+  uint4 kc[2] = {}, kr = {};
+  uint32_t ks[2] = {};
+  auto load_own = [&](const uint8_t* row, bool on) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ld16_or(kc[i], row + 16 * (8 * i + pc), on, kc[i]);
+      ld2_or(ks[i], row + kKv4Codes + 2 * (8 * i + pc), on, ks[i]);
+    }
+    ld16_or(kr, row + kKv4Rope + 16 * pc, on, kr);
+  };
+  int32_t own_next = 0, peer_next = 0;
+  if (warp < kDequantWarps) {
+    const int32_t own = slot_at(0, rank);
+    own_next = slot_at(1, rank);
+    if (!v_own) peer_next = slot_at(0, rank ^ 1u);
+    load_own(row_of(own), true);
+  }
+  cp_async_wait_all();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // barrier inits visible to the partner before any remote operation
@@ -298,73 +322,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
 
   if (warp < kDequantWarps) {
     // ---------------------------------------------------------------- gather and dequantise
-    const uint32_t r7 = (uint32_t)key & 7u, c0 = (uint32_t)(qd & 1) * 4u;
-    const uint32_t blk = (uint32_t)(qd >> 1);
-    uint4 vc[2] = {}, vc_next[2];
-    uint32_t vs[2] = {}, vs_next[2];
-    bool ok = true;
-    for (int it = 0; it <= ntiles && ok; ++it) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDequantRegs));
+    // Within a row's 64-dim block, word j of a piece goes to chunk j ^ (the block's number mod 4) of its half row, so that
+    // the eight threads of a key store to eight different chunks at a time; Q's dims are laid out the same way. In V the
+    // two blocks have the numbers 0 and 1 (the epilogue undoes it), and the partner's keys' words are stored two later.
+    const uint32_t r7 = (uint32_t)key & 7u, h4 = (uint32_t)(pc & 1) * 4u, v_blk = (uint32_t)(pc & 3) >> 1;
+    const uint32_t k_at = base + kSmemK + (uint32_t)(pc >> 1) * kBlock + key * 128 + (((h4 | (uint32_t)(pc >> 1)) ^ r7) << 4);
+    const uint32_t v_at = base + kSmemV + v_blk * kVBlock + ((v_own ? rank : rank ^ 1u) * kOwn + key) * 128 +
+                          (((h4 | (v_blk ^ (v_own ? 0u : 2u))) ^ r7) << 4);
+    const uint32_t r_at = base + kSmemR + key * 128 + (((uint32_t)pc ^ r7) << 4);
+    const uint32_t zero = (uint32_t)a.T >> 16;
+    struct VCodes {
+      uint4 c[2];
+      uint32_t s[2];
+    };
+    // Step `it`: K(it), the loads of K(it + 1) and of V(it), then V(it - 1). False at the end or after a failed wait. All
+    // loads go out in one place and are used a step later (two sets of V's codes, so that none is copied).
+    auto step = [&](const int it, VCodes& next, VCodes& now) -> bool {
       if (it < ntiles) {
-        // K(it): four sub-stages of 128 dims; the RoPE dims go with the last one. (Its buffer, it & 1, is
-        // free: the slot of this sub-stage was last read by S(it - 1), after S(it - 2).)
+        // K(it): two halves of 256 dims; the RoPE dims go with the second one, once S(it - 1), which reads its own
+        // second half and RoPE dims last, is done.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int sub = 4 * it + i, slot = sub % kKSlots;
-          if (sub >= kKSlots && !wait_warp(bar(kBarKEmpty + slot), (sub / kKSlots - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          dequant_piece(kc[i], e4m3x2_to_f16x2(ks[i]), base + kSmemK + slot * kKSlotBytes + blk * kBlock + key * 128, c0, r7);
-          if (i == 3) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t w[4] = {kr[k].x, kr[k].y, kr[k].z, kr[k].w};
-              st_shared_v4(base + kSmemR + (it & 1) * kBlock + key * 128 + (((uint32_t)(2 * qd + k) ^ r7) << 4), w);
-            }
+        for (int i = 0; i < 2; ++i) {
+          const int sub = 2 * it + i, slot = sub % kKSlots;
+          if (sub >= kKSlots && !wait_warp(bar(kBarKEmpty + slot), (sub / kKSlots - 1) & 1, abort_flag)) return false;
+          dequant_piece(kc[i], e4m3x2_to_f16x2(ks[i]), false, k_at + slot * kKSlotBytes);
+          if (i == 1) {
+            const int before = sub - 2;
+            if (it > 0 && !wait_warp(bar(kBarKEmpty + before % kKSlots), (before / kKSlots) & 1, abort_flag)) return false;
+            const uint32_t w[4] = {kr.x, kr.y, kr.z, kr.w};
+            st_shared_v4(r_at, w);
           }
           fence_proxy_async();  // generic-proxy stores, read by the MMA (async proxy)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarKFull + slot));
         }
-        if (!ok) break;
+        // Take delivery of the loads of `now` before the next ones go out: waiting for a load also waits for later
+        // ones that share its scoreboard. (`zero` is 0, which the compiler does not know.)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {  // the pieces of the value dims that this CTA supplies
-          vc_next[j] = rank ? kc[1 + 2 * j] : kc[2 * j];
-          vs_next[j] = rank ? ks[1 + 2 * j] : ks[2 * j];
+        for (int j = 0; j < 2; ++j) {
+          now.c[j].x ^= zero;
+          now.c[j].y ^= zero;
+          now.c[j].z ^= zero;
+          now.c[j].w ^= zero;
+          now.s[j] ^= zero;
         }
-        if (it + 1 < ntiles) {
-          load_own(own_next);
-          own_next = row_at(it + 2, rank);
+        const uint8_t* peer = row_of(peer_next);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // V(it)'s codes: of the partner's row, or this thread's own once more
+          const int piece = 8 * j + 4 * (int)rank + (pc & 3);
+          ld16_or(next.c[j], peer + 16 * piece, !v_own, kc[j]);
+          ld2_or(next.s[j], peer + kKv4Codes + 2 * piece, !v_own, ks[j]);
         }
+        load_own(row_of(own_next), it + 1 < ntiles);
+        own_next = slot_at(it + 2, rank);
+        if (!v_own) peer_next = slot_at(it + 1, rank ^ 1u);
       }
       if (it > 0) {
         // V(it - 1), once PV(it - 2) has read the buffer (for the first tile: once Q has passed through it)
         const int t = it - 1;
-        if (t == 0 && !wait_warp(bar(kBarQFull), 0, abort_flag, rank == 0)) break;
+        if (t == 0 && !wait_warp(bar(kBarQFull), 0, abort_flag, rank == 0)) return false;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          if (t > 0 && !wait_warp(bar(kBarVEmpty + j), (t - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t vb = base + kSmemV + j * kVHalfBytes + blk * kVBlock;
-          dequant_piece(vc[j], without_nan(e4m3x2_to_f16x2(vs[j])), vb + (rank * kOwn + key) * 128, c0, r7);
-          dequant_piece(pc[j], without_nan(e4m3x2_to_f16x2(ps[j])), vb + ((rank ^ 1u) * kOwn + key) * 128, c0, r7);
+          if (t > 0 && !wait_warp(bar(kBarVEmpty + j), (t - 1) & 1, abort_flag)) return false;
+          const uint4 c = now.c[j];
+          dequant_piece(v_own ? c : make_uint4(c.z, c.w, c.x, c.y), without_nan(e4m3x2_to_f16x2(now.s[j])), !v_own,
+                        v_at + j * kVHalfBytes);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarVFull + j));
         }
-        if (!ok) break;
-        if (it < ntiles) {
-          load_peer(peer_next);
-          peer_next = row_at(it + 1, rank ^ 1u);
-        }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        vc[j] = vc_next[j];
-        vs[j] = vs_next[j];
-      }
+      return it < ntiles;
+    };
+    VCodes even = {}, odd = {};
+    for (int it = 0; step(it, even, odd) && step(it + 1, odd, even); it += 2) {
     }
   } else if (warp >= kSWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
@@ -374,32 +406,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         constexpr uint32_t idesc_h = instr_desc(kKeys, false, false), idesc_b = instr_desc(kKeys, true, false);
         bool ok = wait_bar(bar(kBarQFull), 0, abort_flag, true);
         for (int t = 0; t < ntiles && ok; ++t) {
-          if (t > 0) ok = wait_bar(bar(kBarSEmpty), (t - 1) & 1, abort_flag, true);
+          const int sb = t & 1;  // S buffer of tile t
+          if (t > 1) ok = wait_bar(bar(kBarSEmpty + sb), ((t >> 1) - 1) & 1, abort_flag, true);
+          const uint32_t d_s = tmem + kColS + (uint32_t)sb * 64u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int sub = 4 * t + i, slot = sub % kKSlots;
+          for (int i = 0; i < 2; ++i) {
+            const int sub = 2 * t + i, slot = sub % kKSlots;
             if (ok) ok = wait_bar(bar(kBarKFull + slot), (sub / kKSlots) & 1, abort_flag, true);
             if (!ok) break;
             tc_fence_after();
             const uint32_t kb = base + kSmemK + slot * kKSlotBytes;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // 16 dims each
+            for (int k = 0; k < 16; ++k) {  // 16 dims each
               const uint64_t bd = smem_desc(kb + (k >> 2) * kBlock + (k & 3) * 32, 16, 1024);
-              if (i < 3)
-                mma2_tmem_a(tmem + kColS, tmem + kColQ + (i * 8 + k) * 8, bd, idesc_h, (i | k) ? 1u : 0u);
+              const int step = 16 * i + k;
+              if (step < kQTmemDims / 16)
+                mma2_tmem_a(d_s, tmem + kColQ + step * 8, bd, idesc_h, step ? 1u : 0u);
               else
-                mma2_smem_a(tmem + kColS, smem_desc(base + kSmemQ + (k >> 2) * kBlock + (k & 3) * 32, 16, 1024), bd,
-                            idesc_h, 1u);
+                mma2_smem_a(d_s, smem_desc(base + kSmemQ + ((step >> 2) - 4) * kBlock + (step & 3) * 32, 16, 1024),
+                            bd, idesc_h, 1u);
             }
-            if (i == 3) {
+            if (i == 1) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma2_smem_a(tmem + kColS, smem_desc(base + kSmemQ + 2 * kBlock + k * 32, 16, 1024),
-                            smem_desc(base + kSmemR + (t & 1) * kBlock + k * 32, 16, 1024), idesc_b, 1u);
+                mma2_smem_a(d_s, smem_desc(base + kSmemQ + 4 * kBlock + k * 32, 16, 1024),
+                            smem_desc(base + kSmemR + k * 32, 16, 1024), idesc_b, 1u);
             }
             commit_both(bar(kBarKEmpty + slot));
           }
-          if (ok) commit_both(bar(kBarSFull));
+          if (ok) commit_both(bar(kBarSFull + sb));
         }
         // drain: every MMA this thread issued has completed once this barrier flips
         commit_own(bar(kBarDrainS));
@@ -410,16 +445,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         // -------------------------------------------------------------- CTA 1: what S waits for, to CTA 0
         const uint32_t remote = map_to_cta(bar0, 0);
         bool ok = wait_bar(bar(kBarQFull), 0, abort_flag);
-        if (ok) mbar_arrive_remote(remote + 8u * kBarQFull);
+        if (ok) arrive_partner(remote + 8u * kBarQFull);
         for (int t = 0; t < ntiles && ok; ++t) {
-          if (t > 0) {
-            ok = wait_bar(bar(kBarSEmpty), (t - 1) & 1, abort_flag);
-            if (ok) mbar_arrive_remote(remote + 8u * kBarSEmpty);
+          if (t > 1) {
+            ok = wait_bar(bar(kBarSEmpty + (t & 1)), ((t >> 1) - 1) & 1, abort_flag);
+            if (ok) arrive_partner(remote + 8u * (uint32_t)(kBarSEmpty + (t & 1)));
           }
-          for (int i = 0; i < 4 && ok; ++i) {
-            const int sub = 4 * t + i, slot = sub % kKSlots;
+          for (int i = 0; i < 2 && ok; ++i) {
+            const int sub = 2 * t + i, slot = sub % kKSlots;
             ok = wait_bar(bar(kBarKFull + slot), (sub / kKSlots) & 1, abort_flag);
-            if (ok) mbar_arrive_remote(remote + 8u * (uint32_t)(kBarKFull + slot));
+            if (ok) arrive_partner(remote + 8u * (uint32_t)(kBarKFull + slot));
           }
         }
       }
@@ -454,11 +489,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         bool ok = true;
         for (int t = 0; t < ntiles && ok; ++t) {
           ok = wait_bar(bar(kBarVFull), t & 1, abort_flag);
-          if (ok) mbar_arrive_remote(remote + 8u * kBarVFull);
+          if (ok) arrive_partner(remote + 8u * kBarVFull);
           ok = ok && wait_bar(bar(kBarPFull), t & 1, abort_flag);
-          if (ok) mbar_arrive_remote(remote + 8u * kBarPFull);
+          if (ok) arrive_partner(remote + 8u * kBarPFull);
           ok = ok && wait_bar(bar(kBarVFull + 1), t & 1, abort_flag);
-          if (ok) mbar_arrive_remote(remote + 8u * (kBarVFull + 1));
+          if (ok) arrive_partner(remote + 8u * (kBarVFull + 1));
         }
       }
     }
@@ -475,27 +510,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     float* xch = reinterpret_cast<float*>(smem + kSmemX);
     const uint32_t r7 = (uint32_t)r & 7u;
 
-    // Q: each of the two threads brings half of the row (288 dims) into the staging rows and finds its
-    // largest magnitude; then the row, times 2^k, as fp16 into TMEM (both lanes of a row hold all of it)
-    // and shared memory. Row r's 16-byte chunk c lies at c ^ (r & 7) in the staging rows.
+    // Q: the row's largest magnitude (each of its two threads looks at half of it), then the row, times
+    // 2^k, as fp16 into TMEM (both lanes of a row hold all of it) and shared memory.
     float unscale;
     {
-      uint32_t top = 0;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.q + ((int64_t)b * R + (valid ? local_row : 0)) * kDK) + half * 576;
+      __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);
       const uint32_t stage = base + kSmemV + r * (kDK * 2);
+      auto staged = [&](int c) {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stage + (((uint32_t)c ^ r7) << 4)));
+        return v;
+      };
+#pragma unroll 12
+      for (int i = 0; i < kQChunks / 2; ++i) {
+        const uint4 v = staged(half * (kQChunks / 2) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        uint4 v[18];
-#pragma unroll
-        for (int i = 0; i < 18; ++i) v[i] = valid ? ld16(src + (18 * g + i) * 16) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < 18; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w[k] & 0x7fff7fffu);
-          st_shared_v4(stage + (((uint32_t)(half * 36 + 18 * g + i) ^ r7) << 4), w);
-        }
+        for (int k = 0; k < 4; ++k) tops = __hmax2(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
       }
+      uint32_t top = *reinterpret_cast<const uint32_t*>(&tops);
       top = max(top & 0xffffu, top >> 16);
       reinterpret_cast<uint32_t*>(xch)[l128] = top;
       row_pair_sync(q4);
@@ -506,23 +541,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
       k = min(110, k);  // (2^-k stays a normal fp32 number)
       const float up = __int_as_float((127 + k) << 23);
       unscale = __int_as_float((127 - k) << 23) * a.scale_log2;
-      auto staged = [&](int c) {
-        uint4 v;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(stage + (((uint32_t)c ^ r7) << 4)));
-        return v;
-      };
       auto f16_of = [&](uint32_t w) {
         const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
         return *reinterpret_cast<const uint32_t*>(&h);
       };
+      // (chunk i of a 32-dim piece lies at i ^ the number of its 64-dim block mod 4, as K's do)
 #pragma unroll 2
       for (int g = 0; g < kQTmemDims / 32; ++g) {  // 32 dims: 16 columns
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 v = staged(4 * g + i);
+          const uint4 v = staged(4 * g + (i ^ (g >> 1)));
           w[4 * i] = f16_of(v.x);
           w[4 * i + 1] = f16_of(v.y);
           w[4 * i + 2] = f16_of(v.z);
@@ -530,23 +559,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         }
         TMEM_ST16(lane_addr + kColQ + g * 16, w);
       }
-      // chunks 48..63 (dims 384..511) and 64..71 (RoPE): this thread takes every other one
+      // chunks 32..63 (dims 256..511): this thread takes every other piece; then its half of the RoPE dims
+#pragma unroll 2
+      for (int g = half; g < 8; g += 2) {
 #pragma unroll
-      for (int i = 0; i < 12; ++i) {
-        const int c = 2 * i + half;
-        const uint4 v = staged(48 + c);
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = staged(32 + 4 * g + (i ^ (g >> 1)));
+          const uint32_t w[4] = {f16_of(v.x), f16_of(v.y), f16_of(v.z), f16_of(v.w)};
+          st_shared_v4(base + kSmemQ + (g >> 1) * kBlock + r * 128 + (((uint32_t)((g & 1) * 4 + i) ^ r7) << 4), w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 4 * half + i;
+        const uint4 v = staged(64 + c);
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k2 = 0; k2 < 4; ++k2) {
-          if (i < 8) {
-            w[k2] = f16_of(w[k2]);
-          } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[k2] << 16) * up,
-                                                           __uint_as_float(w[k2] & 0xffff0000u) * up);
-            w[k2] = *reinterpret_cast<const uint32_t*>(&h);
-          }
+          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[k2] << 16) * up,
+                                                         __uint_as_float(w[k2] & 0xffff0000u) * up);
+          w[k2] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        st_shared_v4(base + kSmemQ + (c >> 3) * kBlock + r * 128 + (((uint32_t)(c & 7) ^ r7) << 4), w);
+        st_shared_v4(base + kSmemQ + 4 * kBlock + r * 128 + (((uint32_t)c ^ r7) << 4), w);
       }
       fence_proxy_async();
       tmem_wait_st();
@@ -564,16 +598,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     for (int t = 0; t < ntiles; ++t) {
       float sc[64];
       float mt = -INFINITY;
-      if (ok) ok = wait_warp(bar(kBarSFull), t & 1, abort_flag);
+      if (ok) ok = wait_warp(bar(kBarSFull + (t & 1)), (t >> 1) & 1, abort_flag);
       if (ok) {
         tc_fence_after();
         uint32_t(&su)[64] = reinterpret_cast<uint32_t(&)[64]>(sc);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) TMEM_LD16(lane_addr + kColS + c * 16, (su + c * 16));
+        for (int c = 0; c < 4; ++c) TMEM_LD16(lane_addr + kColS + (t & 1) * 64 + c * 16, (su + c * 16));
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarSEmpty));
+        if (lane == 0) mbar_arrive(bar(kBarSEmpty + (t & 1)));
         const int64_t p0 = t0 + (int64_t)t * kKeys + half * 64;  // this thread's first position
         if (p0 + 64 > L) {  // some of them past the prefix: the tree's bitmask
           uint64_t vis = 0;
@@ -663,20 +697,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
       const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
       const int64_t grow = (int64_t)b * R + local_row;
       __half* po = a.part_o + ((int64_t)s * a.rows + (valid ? grow : 0)) * kDLatent + half * 128;
-#pragma unroll 2
-      for (int c = 0; c < 16; ++c) {
-        uint32_t o[16], w[8];
-        TMEM_LD16(lane_addr + kColO + c * 16, o);
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+       for (int blk = 0; blk < 2; ++blk) {
+        const int c = 8 * hf + 4 * blk;
+        uint32_t o[64];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) TMEM_LD16(lane_addr + kColO + (c + u) * 16, (o + 16 * u));
         tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const __half2 h = __floats2half2_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // chunk 2u + k / 4 of the block; in block 1 chunk j lies at j ^ 1
+            const int j = 2 * u + k / 4, at = j ^ blk;
+            const __half2 h = __floats2half2_rn(__uint_as_float(o[8 * at + 2 * (k & 3)]) * inv,
+                                                __uint_as_float(o[8 * at + 2 * (k & 3) + 1]) * inv);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (valid)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                             po + hf * 256 + blk * 64 + u * 16),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
         }
-        if (valid)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + (c >> 3) * 256 + (c & 7) * 16),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                       : "memory");
+       }
       }
       if (half == 0 && local_row < R)
         a.part_lse[(int64_t)s * a.rows + grow] =
