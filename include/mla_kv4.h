@@ -43,7 +43,7 @@ extern "C" {
  * the roundings of the exact quotients. A block whose scale rounds to 0 (max|x| <= 6 * 2^-10)
  * has codes 0; magnitudes over 6 * 448 are held as 2688. A block with a NaN or an infinity gets
  * the scale NaN, so all its dims read as NaN. RoPE dims are copied.
- *   pool      device [num_slots][416] bytes, 16-byte aligned (written).
+ *   pool      device [num_slots][416] bytes, 32-byte aligned (written).
  *   rows      device bf16, row i at rows + i * row_stride elements; 16-byte aligned; row_stride
  *             >= 576 and a multiple of 8 (rows may be a slice of a wider projection's output).
  *   slot_map  device int32 [num_rows]; -1 skips the row (padding). Another value outside
@@ -69,7 +69,7 @@ int mla_kv4_gather(const void *pool, int64_t num_slots, const int32_t *slots, in
  * their first 512. num_nodes = 1 with tree_parent -1 is single-token decode.
  *   desc        as for mla_verify_attn; num_slots counts pool rows. MLA_FLAG_PREFIX_STABLE is
  *               accepted and changes nothing; MLA_FLAG_SIMT runs the plain reference kernel.
- *   pool        device [num_slots][416] bytes, 16-byte aligned.
+ *   pool        device [num_slots][416] bytes, 32-byte aligned.
  *   tree_sizes  NULL (every tree has desc->num_nodes nodes), or device int32 [B] as for
  *               mla_verify_attn_ragged: rows of nodes >= tree_sizes[b] give out = 0, lse = -inf.
  *   workspace   device, >= mla_verify_kv4_workspace_size bytes, 256-byte aligned.

@@ -100,7 +100,7 @@ extern "C" int mla_verify_attn_kv4(const mla_verify_desc* d, const void* q, cons
   if (rc) return rc;
   if (!q || !pool || !slot_table || !seq_lens || !tree_parent || !out || !lse || !workspace)
     return MLA_ERR_INVALID_ARGUMENT;
-  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256) ||
+  if (!aligned(q, 16) || !aligned(pool, 32) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256) ||
       !aligned(slot_table, 4) || !aligned(seq_lens, 4) || !aligned(tree_sizes, 4) || !aligned(tree_parent, 4))
     return MLA_ERR_INVALID_ARGUMENT;
   const bool debug = (d->flags & MLA_FLAG_DEBUG_CHECKS) != 0;

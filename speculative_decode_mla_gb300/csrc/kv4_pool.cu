@@ -155,7 +155,7 @@ int check_rows(const void* pool, int64_t num_slots, const int32_t* slots, int64_
   if (num_slots < 1 || num_slots > 0x7fffffff || num_rows < 0) return MLA_ERR_INVALID_ARGUMENT;
   if ((num_rows + kRowsPerBlock - 1) / kRowsPerBlock > 0x7fffffff) return MLA_ERR_INVALID_ARGUMENT;
   if (num_rows > 0 && (!pool || !slots)) return MLA_ERR_INVALID_ARGUMENT;
-  if (!aligned(pool, 16) || !aligned(slots, 4)) return MLA_ERR_INVALID_ARGUMENT;
+  if (!aligned(pool, 32) || !aligned(slots, 4)) return MLA_ERR_INVALID_ARGUMENT;
   if (debug && !dev_status) return MLA_ERR_INVALID_ARGUMENT;
   return MLA_OK;
 }

@@ -21,7 +21,7 @@
 //                keys), then, one tile later, V. A value's codes are read once for both.
 //   warps 16-19  softmax, two threads a row (64 keys each): S from TMEM, ancestor bitmask on tree positions, row
 //                maximum over the two threads through shared memory, exp2, P (fp16) to shared memory; O is
-//                rescaled only when the running maximum grows by more than 2^8. Epilogue: O / l to the workspace.
+//                rescaled only when the running maximum grows by more than 2^8. The dequantising warps write O / l.
 //   warp 20, 21  one thread each: CTA 0 issues S and PV for the pair; CTA 1 tells CTA 0 what is ready
 //                (local barriers, then one remote arrive each: a cluster-scope release is slow, so the
 //                working warps stay off it).
@@ -62,8 +62,6 @@ constexpr int kSmemX = kSmemQ + 5 * kBlock;             // exchange between the 
 constexpr int kSmemBar = kSmemX + 1024;
 constexpr int kSmemBytes = kSmemBar + 512 + 1024;       // barriers, TMEM slot, tree parents + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory");
-// Q's rows pass through V and P on their way in (64 rows x 1152 bytes)
-static_assert(2 * kVHalfBytes + 2 * kBlock >= kCtaRows * kDK * 2, "Q staging");
 
 constexpr int kDequantWarps = 16;
 constexpr int kSWarp = 20, kPVWarp = 21;  // 16..19: softmax, TMEM lane quarters 0..3; 22 and 23 only fill the warpgroup
@@ -76,7 +74,7 @@ constexpr int kParentThread0 = kSWarp * 32;  // 64 threads read the tree parents
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256 /* two buffers of 64 */, kColQ = 384;
 constexpr int kQTmemDims = 256;
-constexpr int kQChunks = kDK * 2 / 16;  // 72 16-byte chunks of a query row
+static_assert(2 * kVHalfBytes >= kCtaRows * kQTmemDims * 2, "half of Q passes through V's place");
 constexpr float kPBias = 7.f;
 
 constexpr int kBarKFull = 0, kBarKEmpty = kKSlots, kBarVFull = 2 * kKSlots /*2*/, kBarVEmpty = kBarVFull + 2 /*2*/,
@@ -119,21 +117,42 @@ __device__ __forceinline__ void commit_own(uint32_t bar) {
       "h"((uint16_t)1)
       : "memory");
 }
-// v = *p where `on`, else v = other (16 bytes, and 2 bytes widened). The registers are read and written by one
+// A row's 64 dims as a thread takes them: 32 bytes of codes (two pieces of 32 dims) and their four scales.
+struct Codes {
+  uint32_t c[8];
+  uint32_t s;
+};
+// v = the codes and scales at *p and *q where `on`, else v = other. The registers are read and written by one
 // predicated instruction each: a load that reaches the next iteration through a branch gets a copy at the
 // branch's end, and the copy waits for the load (about 1700 cycles a tile).
-__device__ __forceinline__ void ld16_or(uint4& v, const uint8_t* p, bool on, uint4 other) {
+__device__ __forceinline__ void load_codes_or(Codes& v, const uint8_t* p, const uint8_t* q, bool on, const Codes& other) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %11, 0;\n"
+      "@!p mov.b32 %0, %12;\n@!p mov.b32 %1, %13;\n@!p mov.b32 %2, %14;\n@!p mov.b32 %3, %15;\n"
+      "@!p mov.b32 %4, %16;\n@!p mov.b32 %5, %17;\n@!p mov.b32 %6, %18;\n@!p mov.b32 %7, %19;\n"
+      "@!p mov.b32 %8, %20;\n"
+      "@p ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%9];\n"
+      "@p ld.global.nc.b32 %8, [%10];\n}"
+      : "+r"(v.c[0]), "+r"(v.c[1]), "+r"(v.c[2]), "+r"(v.c[3]), "+r"(v.c[4]), "+r"(v.c[5]), "+r"(v.c[6]), "+r"(v.c[7]),
+        "+r"(v.s)
+      : "l"(p), "l"(q), "r"((int)on), "r"(other.c[0]), "r"(other.c[1]), "r"(other.c[2]), "r"(other.c[3]), "r"(other.c[4]),
+        "r"(other.c[5]), "r"(other.c[6]), "r"(other.c[7]), "r"(other.s));
+}
+__device__ __forceinline__ void load_codes_if(Codes& v, const uint8_t* p, const uint8_t* q, bool on) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %11, 0;\n"
+      "@p ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%9];\n"
+      "@p ld.global.nc.b32 %8, [%10];\n}"
+      : "+r"(v.c[0]), "+r"(v.c[1]), "+r"(v.c[2]), "+r"(v.c[3]), "+r"(v.c[4]), "+r"(v.c[5]), "+r"(v.c[6]), "+r"(v.c[7]),
+        "+r"(v.s)
+      : "l"(p), "l"(q), "r"((int)on));
+}
+__device__ __forceinline__ void ld16_if(uint32_t (&v)[4], const uint8_t* p, bool on) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n"
-      "@!p mov.b32 %0, %6;\n@!p mov.b32 %1, %7;\n@!p mov.b32 %2, %8;\n@!p mov.b32 %3, %9;\n"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(p), "r"((int)on), "r"(other.x), "r"(other.y), "r"(other.z), "r"(other.w));
-}
-__device__ __forceinline__ void ld2_or(uint32_t& v, const uint8_t* p, bool on, uint32_t other) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@!p mov.b32 %0, %3;\n@p ld.global.nc.u16 %0, [%1];\n}"
-               : "+r"(v)
-               : "l"(p), "r"((int)on), "r"(other));
+      "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
+      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])
+      : "l"(p), "r"((int)on));
 }
 // Arrives on a barrier of the partner CTA. What this thread has acquired from its own CTA's barriers is shared
 // memory, so the release is restricted to that; a full cluster-scope release took about 1500 cycles.
@@ -150,9 +169,8 @@ __device__ __forceinline__ void row_pair_sync(int softmax_warp) {
 // 32 values (a 16-byte piece of a row's codes, its two scales as fp16; word j = 8 values) into four 16-byte chunks of
 // a 128-byte row: word j at `at` ^ 16 j, where `at` is the place of word 0 (128B swizzle: chunk c lies at c ^ (row & 7)).
 // `swap`: the words come in the order 2, 3, 0, 1, so the scales change places.
-__device__ __forceinline__ void dequant_piece(uint4 code, uint32_t scales, bool swap, uint32_t at) {
+__device__ __forceinline__ void dequant_piece(const uint32_t* w, uint32_t scales, bool swap, uint32_t at) {
   const uint32_t s0 = __byte_perm(scales, 0, swap ? 0x3232 : 0x1010), s1 = __byte_perm(scales, 0, swap ? 0x1010 : 0x3232);
-  const uint32_t w[4] = {code.x, code.y, code.z, code.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t h[4];
@@ -258,27 +276,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
 
-  // Q: the CTA's 64 rows into staging rows (V's and P's place), 16-byte chunk c of row r at c ^ (r & 7); rows of
-  // padding nodes and past the sequence are zeros.
-  {
-    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + ((int64_t)b * R + row0) * kDK);
-    const int rows = max(0, min(kCtaRows, min(R, Tb * a.H) - row0));
-    for (int i = threadIdx.x; i < kCtaRows * kQChunks; i += kThreads) {
-      const int r = i / kQChunks, c = i % kQChunks;
-      const uint32_t dst = base + kSmemV + r * (kDK * 2) + ((uint32_t)(c ^ (r & 7)) << 4);
-      if (r < rows) {
-        cp_async16(dst, q + (int64_t)i * 16);
-      } else {
-        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-        st_shared_v4(dst, zero);
-      }
-    }
-  }
-
   // ------------------------------------------------------------------ what the gather needs first
-  // Eight threads a key: thread (key, pc) with key = 4 warp + lane / 8, pc = lane % 8. For K it takes the pieces (32 dims)
-  // 8i + pc of its own key's row, i < 2. For V (the dims of pieces 8j + 4 rank + pc % 4) the threads with pc / 4 == rank use
-  // the same codes again, the others take the partner's key. A load of a warp is then four runs of 128 bytes.
+  // Eight threads a key: thread (key, pc) with key = 4 warp + lane / 8, pc = lane % 8 takes 32 bytes of its own key's
+  // codes: the pieces (32 dims) 2 pc + i, i < 2, of K's half i. For V (CTA r supplies the dims 256 r .. 256 r + 255, of
+  // half j the pieces 8 r + 2x + j) the threads with pc / 4 == rank use the same codes again, the others take the
+  // partner's key.
   const int key = warp * 4 + (lane >> 3), pc = lane & 7;
   const bool v_own = (pc >> 2) == (int)rank;
   const uint8_t* pool = reinterpret_cast<const uint8_t*>(a.kv);
@@ -296,27 +298,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     }
     return pool + (int64_t)slot * kKv4Row;
   };
-  uint4 kc[2] = {}, kr = {};
-  uint32_t ks[2] = {};
+  Codes kc = {};
+  uint32_t kr[4] = {};
   auto load_own = [&](const uint8_t* row, bool on) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ld16_or(kc[i], row + 16 * (8 * i + pc), on, kc[i]);
-      ld2_or(ks[i], row + kKv4Codes + 2 * (8 * i + pc), on, ks[i]);
-    }
-    ld16_or(kr, row + kKv4Rope + 16 * pc, on, kr);
+    load_codes_if(kc, row + 32 * pc, row + kKv4Codes + 4 * pc, on);
+    ld16_if(kr, row + kKv4Rope + 16 * pc, on);
   };
   int32_t own_next = 0, peer_next = 0;
   if (warp < kDequantWarps) {
     const int32_t own = slot_at(0, rank);
     own_next = slot_at(1, rank);
     if (!v_own) peer_next = slot_at(0, rank ^ 1u);
+    // Q: the same eight threads take query row `key`, 16-byte chunks pc + 8m (rows of padding nodes and past the
+    // sequence: zeros). Their largest magnitude gives the row's power of two; times it, the dims of K's half 0 go
+    // as fp16 to staging rows in V's place (the softmax warps put them into TMEM), those of half 1 and the RoPE dims
+    // to their places.
+    const bool q_valid = row0 + key < min(R, Tb * a.H);
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(a.q + ((int64_t)b * R + (q_valid ? row0 + key : 0)) * kDK) + 16 * pc;
+    uint32_t qv[9][4] = {};
+#pragma unroll
+    for (int m = 0; m < 9; ++m) ld16_if(qv[m], q + 128 * m, q_valid);
     load_own(row_of(own), true);
+    __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int m = 0; m < 9; ++m)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tops = __hmax2(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&qv[m][k])));
+    uint32_t top = *reinterpret_cast<const uint32_t*>(&tops);
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // top is in [2^(e - 127), 2^(e - 126)): k = 14 - (e - 127); rows of zeros, infinities or NaN stay as they are
+    const int e = (int)(top >> 7);
+    const int k2 = min(110, (e == 0 || e == 255) ? 0 : 141 - e);  // (2^-k2 stays a normal fp32 number)
+    const float up = __int_as_float((127 + k2) << 23);
+    if (pc == 0) reinterpret_cast<float*>(smem + kSmemX)[key] = __int_as_float((127 - k2) << 23) * a.scale_log2;
+    const uint32_t r7 = (uint32_t)key & 7u, jj = (uint32_t)pc & 3u;
+#pragma unroll
+    for (int m = 0; m < 9; ++m) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float lo = __uint_as_float(qv[m][k] << 16) * up, hi = __uint_as_float(qv[m][k] & 0xffff0000u) * up;
+        if (m < 8) {
+          const __half2 h = __floats2half2_rn(lo, hi);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      // chunk pc + 8m is word jj of piece 2m + pc / 4: half pc / 4, block m / 2, half row m % 2
+      const uint32_t c = jj ^ (uint32_t)(m >> 1);
+      uint32_t at = base + kSmemV + key * 512 + (((uint32_t)(4 * m) + c) ^ r7) * 16;
+      if (pc >= 4) at = base + kSmemQ + (m >> 1) * kBlock + key * 128 + (((uint32_t)(4 * (m & 1)) + c) ^ r7) * 16;
+      if (m == 8) at = base + kSmemQ + 4 * kBlock + key * 128 + ((uint32_t)pc ^ r7) * 16;
+      st_shared_v4(at, w);
+    }
+    fence_proxy_async();  // generic-proxy stores, read by the MMA (async proxy)
   }
-  cp_async_wait_all();
+
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // barrier inits visible to the partner before any remote operation
+  // Barrier inits (released by the fence after them) visible to the partner before any remote operation; the arrival is
+  // relaxed, so it does not wait for the loads in flight.
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -332,13 +379,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
                           (((h4 | (v_blk ^ (v_own ? 0u : 2u))) ^ r7) << 4);
     const uint32_t r_at = base + kSmemR + key * 128 + (((uint32_t)pc ^ r7) << 4);
     const uint32_t zero = (uint32_t)a.T >> 16;
-    struct VCodes {
-      uint4 c[2];
-      uint32_t s[2];
-    };
     // Step `it`: K(it), the loads of K(it + 1) and of V(it), then V(it - 1). False at the end or after a failed wait. All
     // loads go out in one place and are used a step later (two sets of V's codes, so that none is copied).
-    auto step = [&](const int it, VCodes& next, VCodes& now) -> bool {
+    auto step = [&](const int it, Codes& next, Codes& now) -> bool {
       if (it < ntiles) {
         // K(it): two halves of 256 dims; the RoPE dims go with the second one, once S(it - 1), which reads its own
         // second half and RoPE dims last, is done.
@@ -346,12 +389,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         for (int i = 0; i < 2; ++i) {
           const int sub = 2 * it + i, slot = sub % kKSlots;
           if (sub >= kKSlots && !wait_warp(bar(kBarKEmpty + slot), (sub / kKSlots - 1) & 1, abort_flag)) return false;
-          dequant_piece(kc[i], e4m3x2_to_f16x2(ks[i]), false, k_at + slot * kKSlotBytes);
+          dequant_piece(kc.c + 4 * i, e4m3x2_to_f16x2(i ? kc.s >> 16 : kc.s), false, k_at + slot * kKSlotBytes);
           if (i == 1) {
             const int before = sub - 2;
             if (it > 0 && !wait_warp(bar(kBarKEmpty + before % kKSlots), (before / kKSlots) & 1, abort_flag)) return false;
-            const uint32_t w[4] = {kr.x, kr.y, kr.z, kr.w};
-            st_shared_v4(r_at, w);
+            st_shared_v4(r_at, kr);
           }
           fence_proxy_async();  // generic-proxy stores, read by the MMA (async proxy)
           __syncwarp();
@@ -360,20 +402,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         // Take delivery of the loads of `now` before the next ones go out: waiting for a load also waits for later
         // ones that share its scoreboard. (`zero` is 0, which the compiler does not know.)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          now.c[j].x ^= zero;
-          now.c[j].y ^= zero;
-          now.c[j].z ^= zero;
-          now.c[j].w ^= zero;
-          now.s[j] ^= zero;
-        }
-        const uint8_t* peer = row_of(peer_next);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {  // V(it)'s codes: of the partner's row, or this thread's own once more
-          const int piece = 8 * j + 4 * (int)rank + (pc & 3);
-          ld16_or(next.c[j], peer + 16 * piece, !v_own, kc[j]);
-          ld2_or(next.s[j], peer + kKv4Codes + 2 * piece, !v_own, ks[j]);
-        }
+        for (int j = 0; j < 8; ++j) now.c[j] ^= zero;
+        now.s ^= zero;
+        const uint8_t* peer = row_of(peer_next);  // V(it)'s codes: of the partner's row, or this thread's own once more
+        load_codes_or(next, peer + 32 * (4 * (int)rank + (pc & 3)), peer + kKv4Codes + 4 * (4 * (int)rank + (pc & 3)), !v_own, kc);
         load_own(row_of(own_next), it + 1 < ntiles);
         own_next = slot_at(it + 2, rank);
         if (!v_own) peer_next = slot_at(it + 1, rank ^ 1u);
@@ -385,9 +417,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (t > 0 && !wait_warp(bar(kBarVEmpty + j), (t - 1) & 1, abort_flag)) return false;
-          const uint4 c = now.c[j];
-          dequant_piece(v_own ? c : make_uint4(c.z, c.w, c.x, c.y), without_nan(e4m3x2_to_f16x2(now.s[j])), !v_own,
-                        v_at + j * kVHalfBytes);
+          const uint32_t* c = now.c + 4 * j;
+          const uint32_t w[4] = {v_own ? c[0] : c[2], v_own ? c[1] : c[3], v_own ? c[2] : c[0], v_own ? c[3] : c[1]};
+          dequant_piece(w, without_nan(e4m3x2_to_f16x2(j ? now.s >> 16 : now.s)), !v_own, v_at + j * kVHalfBytes);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarVFull + j));
@@ -395,8 +427,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
       }
       return it < ntiles;
     };
-    VCodes even = {}, odd = {};
+    Codes even = {}, odd = {};
     for (int it = 0; step(it, even, odd) && step(it + 1, odd, even); it += 2) {
+    }
+
+    // Epilogue: O / l as fp16 partials. Warp w reads TMEM lanes 32 (w % 4) .. (rows lane & 63) and the 64-dim block
+    // w / 4 % 2 of half w / 8; lanes from 64 on hold the dims of CTA 1's V.
+    const bool done = wait_warp(bar(kBarPEmpty), (ntiles - 1) & 1, abort_flag);
+    asm volatile("bar.sync 3, %0;" ::"n"(32 * (kDequantWarps + 4)) : "memory");
+    if (done) {
+      tc_fence_after();
+      const int l128 = (warp & 3) * 32 + lane, r = l128 & 63, local_row = row0 + r, hf = warp >> 3, blk = (warp >> 2) & 1;
+      const bool valid = local_row < R && local_row / a.H < Tb;
+      const float inv = reinterpret_cast<const float*>(smem + kSmemX)[(~ntiles & 1) * 128 + r];
+      __half* po = a.part_o + ((int64_t)s * a.rows + (valid ? (int64_t)b * R + local_row : 0)) * kDLatent +
+                   (l128 >> 6) * 256 + 128 * blk + 32 * hf;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // piece 2 (2 blk + h) + hf of this half's 256 dims
+        uint32_t o[32];
+        TMEM_LD16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColO + hf * 128 + blk * 64 + h * 32, o);
+        TMEM_LD16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColO + hf * 128 + blk * 64 + h * 32 + 16, (o + 16));
+        tmem_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const __half2 v = __floats2half2_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          w[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < 16; k += 8) {  // chunk j of block 1 lies at j ^ 1
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + 64 * h + 2 * k),
+                         "r"(blk ? w[k + 4] : w[k]), "r"(blk ? w[k + 5] : w[k + 1]), "r"(blk ? w[k + 6] : w[k + 2]),
+                         "r"(blk ? w[k + 7] : w[k + 3]), "r"(blk ? w[k] : w[k + 4]), "r"(blk ? w[k + 1] : w[k + 5]),
+                         "r"(blk ? w[k + 2] : w[k + 6]), "r"(blk ? w[k + 3] : w[k + 7])
+                         : "memory");
+          }
+        }
+      }
     }
   } else if (warp >= kSWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
@@ -510,84 +578,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     float* xch = reinterpret_cast<float*>(smem + kSmemX);
     const uint32_t r7 = (uint32_t)r & 7u;
 
-    // Q: the row's largest magnitude (each of its two threads looks at half of it), then the row, times
-    // 2^k, as fp16 into TMEM (both lanes of a row hold all of it) and shared memory.
-    float unscale;
-    {
-      __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);
-      const uint32_t stage = base + kSmemV + r * (kDK * 2);
-      auto staged = [&](int c) {
-        uint4 v;
+    // Q's half 0 into TMEM, from the staging rows (both lanes of a row hold all of it)
+    const float unscale = xch[r];
+#pragma unroll 4
+    for (int g = 0; g < kQTmemDims / 32; ++g) {  // 32 dims: 16 columns
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(stage + (((uint32_t)c ^ r7) << 4)));
-        return v;
-      };
-#pragma unroll 12
-      for (int i = 0; i < kQChunks / 2; ++i) {
-        const uint4 v = staged(half * (kQChunks / 2) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tops = __hmax2(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
-      }
-      uint32_t top = *reinterpret_cast<const uint32_t*>(&tops);
-      top = max(top & 0xffffu, top >> 16);
-      reinterpret_cast<uint32_t*>(xch)[l128] = top;
-      row_pair_sync(q4);
-      top = max(top, reinterpret_cast<uint32_t*>(xch)[l128 ^ 64]);
-      // top is in [2^(e - 127), 2^(e - 126)): k = 14 - (e - 127); rows of zeros, infinities or NaN stay as they are
-      const int e = (int)(top >> 7);
-      int k = (e == 0 || e == 255) ? 0 : 141 - e;
-      k = min(110, k);  // (2^-k stays a normal fp32 number)
-      const float up = __int_as_float((127 + k) << 23);
-      unscale = __int_as_float((127 - k) << 23) * a.scale_log2;
-      auto f16_of = [&](uint32_t w) {
-        const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-        return *reinterpret_cast<const uint32_t*>(&h);
-      };
-      // (chunk i of a 32-dim piece lies at i ^ the number of its 64-dim block mod 4, as K's do)
-#pragma unroll 2
-      for (int g = 0; g < kQTmemDims / 32; ++g) {  // 32 dims: 16 columns
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = staged(4 * g + (i ^ (g >> 1)));
-          w[4 * i] = f16_of(v.x);
-          w[4 * i + 1] = f16_of(v.y);
-          w[4 * i + 2] = f16_of(v.z);
-          w[4 * i + 3] = f16_of(v.w);
-        }
-        TMEM_ST16(lane_addr + kColQ + g * 16, w);
-      }
-      // chunks 32..63 (dims 256..511): this thread takes every other piece; then its half of the RoPE dims
-#pragma unroll 2
-      for (int g = half; g < 8; g += 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = staged(32 + 4 * g + (i ^ (g >> 1)));
-          const uint32_t w[4] = {f16_of(v.x), f16_of(v.y), f16_of(v.z), f16_of(v.w)};
-          st_shared_v4(base + kSmemQ + (g >> 1) * kBlock + r * 128 + (((uint32_t)((g & 1) * 4 + i) ^ r7) << 4), w);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 4 * half + i;
-        const uint4 v = staged(64 + c);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k2 = 0; k2 < 4; ++k2) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[k2] << 16) * up,
-                                                         __uint_as_float(w[k2] & 0xffff0000u) * up);
-          w[k2] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        st_shared_v4(base + kSmemQ + 4 * kBlock + r * 128 + (((uint32_t)c ^ r7) << 4), w);
-      }
-      fence_proxy_async();
-      tmem_wait_st();
-      tc_fence_before();
-      row_pair_sync(q4);  // the staging rows (and xch) have been read by both
-      if (lane == 0) mbar_arrive(bar(kBarQFull));
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "r"(base + kSmemV + r * 512 + (((uint32_t)(4 * g + i) ^ r7) << 4)));
+      TMEM_ST16(lane_addr + kColQ + g * 16, w);
     }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarQFull));
 
     uint64_t anc = 0;  // anc*(node): the tree positions this row can see
     if (valid)
@@ -687,47 +693,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
       if (lane == 0) mbar_arrive(bar(kBarPFull));
     }
 
-    // epilogue: O / l as fp16 partials, 256 dims a thread in runs of 128; lse
+    // l of the row from its two threads; 1 / l for the warps that write O, lse to the workspace
     xch[(ntiles & 1) * 128 + l128] = l_run;
     row_pair_sync(q4);
     const float l = l_run + xch[(ntiles & 1) * 128 + (l128 ^ 64)];
-    if (ok) ok = wait_warp(bar(kBarPEmpty), (ntiles - 1) & 1, abort_flag);
-    if (ok) {
-      tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-      const int64_t grow = (int64_t)b * R + local_row;
-      __half* po = a.part_o + ((int64_t)s * a.rows + (valid ? grow : 0)) * kDLatent + half * 128;
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-       for (int blk = 0; blk < 2; ++blk) {
-        const int c = 8 * hf + 4 * blk;
-        uint32_t o[64];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) TMEM_LD16(lane_addr + kColO + (c + u) * 16, (o + 16 * u));
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // chunk 2u + k / 4 of the block; in block 1 chunk j lies at j ^ 1
-            const int j = 2 * u + k / 4, at = j ^ blk;
-            const __half2 h = __floats2half2_rn(__uint_as_float(o[8 * at + 2 * (k & 3)]) * inv,
-                                                __uint_as_float(o[8 * at + 2 * (k & 3) + 1]) * inv);
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          if (valid)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                             po + hf * 256 + blk * 64 + u * 16),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                         : "memory");
-        }
-       }
-      }
-      if (half == 0 && local_row < R)
-        a.part_lse[(int64_t)s * a.rows + grow] =
+    if (half == 0) {
+      xch[(~ntiles & 1) * 128 + r] = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+      if (ok && local_row < R)
+        a.part_lse[(int64_t)s * a.rows + (int64_t)b * R + local_row] =
             !valid || l == 0.f ? -INFINITY : (m_run + (log2f(l) - kPBias)) * 0.6931471805599453f;
     }
+    __syncwarp();
+    asm volatile("bar.arrive 3, %0;" ::"n"(32 * (kDequantWarps + 4)) : "memory");
   }
 
   // ---------------------------------------------------------------- teardown

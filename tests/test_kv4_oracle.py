@@ -89,7 +89,7 @@ FAKE = 1 << 20
 def test_append_and_gather_refuse(lib):
     f = lib.mla_kv4_append
     ok = [FAKE, 10, FAKE, 576, FAKE, 4, 0, None, None]
-    bad = [(0, None), (0, FAKE + 8), (1, 0), (1, 1 << 31), (2, None), (2, FAKE + 2), (3, 575), (3, 580), (4, None), (4, FAKE + 2),
+    bad = [(0, None), (0, FAKE + 16), (1, 0), (1, 1 << 31), (2, None), (2, FAKE + 2), (3, 575), (3, 580), (4, None), (4, FAKE + 2),
            (5, -1), (6, 1)]
     for i, v in bad:
         args = list(ok)
@@ -98,7 +98,7 @@ def test_append_and_gather_refuse(lib):
     assert f(None, 10, None, 576, None, 0, 0, None, None) == 0        # no rows: nothing to do
     g = lib.mla_kv4_gather
     ok = [FAKE, 10, FAKE, 4, FAKE, 0, None, None]
-    for i, v in [(0, None), (0, FAKE + 4), (1, 0), (2, None), (2, FAKE + 1), (3, -2), (4, None), (4, FAKE + 8), (5, 1)]:
+    for i, v in [(0, None), (0, FAKE + 16), (1, 0), (2, None), (2, FAKE + 1), (3, -2), (4, None), (4, FAKE + 8), (5, 1)]:
         args = list(ok)
         args[i] = v
         assert g(*args) == -1, (i, v)
@@ -138,6 +138,9 @@ def test_verify_kv4_refuses(lib):
             args = list(ok)
             args[i] = v
             assert f(ctypes.byref(d), *args) == -1, (i, v)
+    args = list(ok)
+    args[1] = FAKE + 16                         # the pool's alignment is 32
+    assert f(ctypes.byref(d), *args) == -1
     args = list(ok)
     args[4] = FAKE + 2
     assert f(ctypes.byref(d), *args) == -1
