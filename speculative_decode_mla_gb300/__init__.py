@@ -295,10 +295,12 @@ def kv_compact(src_pool, dst_pool, slot_table, seq_lens, dst_base, *, num_nodes:
     return dst_pool, new_slot_table
 
 
-def _check_tensor(name: str, t, dtype, shape, device):
-    """A contiguous CUDA tensor of this type, shape (None: any extent) and device, or ValueError."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}: got {t.dtype} on {t.device}")
+def _check_tensor(name: str, t, dtype, shape, device: int):
+    """A contiguous tensor of this type and shape (None: any extent) on CUDA device `device`, or ValueError."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
+        return
+    if not t.is_cuda or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}: got {t.dtype} on {t.device}")
     if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name} must have the shape {tuple(shape)}: got {tuple(t.shape)}")
 
@@ -306,17 +308,20 @@ def _check_tensor(name: str, t, dtype, shape, device):
 _HERE = contextlib.nullcontext()
 
 
-def _on(device, stream):
-    """(stream, context): the context makes the device and the stream current, so that what a call
+def _on(device: int, stream):
+    """(raw stream, context): the context makes the device and the stream current, so that what a call
     allocates belongs to the stream that its kernels run on."""
     import torch
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-        if torch.cuda.current_device() == device.index:
-            return stream, _HERE
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    return stream, torch.cuda.stream(stream)
+        raw = torch._C._cuda_getCurrentRawStream(device)
+        if torch.cuda.current_device() == device:
+            return raw, _HERE
+        return raw, torch.cuda.device(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def slot_map_build(seq_lens, new_lens, free_pages, free_count, slot_table, *, page_size: int, num_pages: int,
@@ -329,35 +334,47 @@ def slot_map_build(seq_lens, new_lens, free_pages, free_count, slot_table, *, pa
     Returns (slot_map [map_capacity], cu_new [B + 1], held_out [B], free_left [1]); each may be passed in.
     """
     import torch
-    dev, B, i32 = seq_lens.device, seq_lens.shape[0], torch.int32
+    dev, B, i32 = seq_lens.get_device(), seq_lens.shape[0], torch.int32
     if map_capacity is None:
         if slot_map is None:
             raise ValueError("map_capacity or slot_map is needed")
         map_capacity = slot_map.numel()
-    s, here = _on(dev, stream)
+    raw, here = _on(dev, stream)
+    slots_wide, blocks_wide = slot_table.shape[-1], 0 if block_table is None else block_table.shape[-1]
+    _check_tensor("seq_lens", seq_lens, i32, (B,), dev)
+    _check_tensor("new_lens", new_lens, i32, (B,), dev)
+    _check_tensor("free_pages", free_pages, i32, (free_pages.numel(),), dev)
+    _check_tensor("free_count", free_count, i32, (1,), dev)
+    _check_tensor("slot_table", slot_table, i32, (B, slots_wide), dev)
+    if held_lens is not None:
+        _check_tensor("held_lens", held_lens, i32, (B,), dev)
+    if block_table is not None:
+        _check_tensor("block_table", block_table, i32, (B, blocks_wide), dev)
+    if dev_status is not None:
+        _check_tensor("dev_status", dev_status, i32, (1,), dev)
     with here:
+        like = seq_lens.device
         if slot_map is None:
-            slot_map = torch.empty(map_capacity, dtype=i32, device=dev)
+            slot_map = torch.empty(map_capacity, dtype=i32, device=like)
+        else:
+            _check_tensor("slot_map", slot_map, i32, (map_capacity,), dev)
         if cu_new is None:
-            cu_new = torch.empty(B + 1, dtype=i32, device=dev)
+            cu_new = torch.empty(B + 1, dtype=i32, device=like)
+        else:
+            _check_tensor("cu_new", cu_new, i32, (B + 1,), dev)
         if held_out is None:
-            held_out = torch.empty(B, dtype=i32, device=dev)
+            held_out = torch.empty(B, dtype=i32, device=like)
+        else:
+            _check_tensor("held_out", held_out, i32, (B,), dev)
         if free_left is None:
-            free_left = torch.empty(1, dtype=i32, device=dev)
-        for name, t, shape in (("seq_lens", seq_lens, (B,)), ("new_lens", new_lens, (B,)), ("held_lens", held_lens, (B,)),
-                               ("free_pages", free_pages, (None,)), ("free_count", free_count, (1,)),
-                               ("slot_table", slot_table, (B, None)), ("block_table", block_table, (B, None)),
-                               ("slot_map", slot_map, (map_capacity,)), ("cu_new", cu_new, (B + 1,)),
-                               ("held_out", held_out, (B,)), ("free_left", free_left, (1,)),
-                               ("dev_status", dev_status, (1,))):
-            if t is not None:
-                _check_tensor(name, t, i32, shape, dev)
+            free_left = torch.empty(1, dtype=i32, device=like)
+        else:
+            _check_tensor("free_left", free_left, i32, (1,), dev)
         rc = load_library().mla_slot_map_build(
             seq_lens.data_ptr(), new_lens.data_ptr(), _ptr_or_none(held_lens), B, page_size, num_pages,
             free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), _ptr_or_none(block_table),
-            0 if block_table is None else block_table.shape[1], slot_table.data_ptr(), slot_table.shape[1],
-            slot_map.data_ptr(), map_capacity, cu_new.data_ptr(), held_out.data_ptr(), free_left.data_ptr(), int(debug),
-            _ptr_or_none(dev_status), s.cuda_stream)
+            blocks_wide, slot_table.data_ptr(), slots_wide, slot_map.data_ptr(), map_capacity, cu_new.data_ptr(),
+            held_out.data_ptr(), free_left.data_ptr(), int(debug), _ptr_or_none(dev_status), raw)
     _check(rc, "mla_slot_map_build")
     return slot_map, cu_new, held_out, free_left
 
@@ -366,20 +383,20 @@ def kv4_append(pool, rows, slot_map, *, debug: bool = False, dev_status=None, st
     """Quantise bf16 rows [n, 576] (rows may be strided, dims contiguous) into pool[slot_map[i]] of the 4-bit pool
     uint8 [slots, 416] (``include/mla_kv4.h``); slot -1 skips a row. In place on pool."""
     import torch
-    dev, n = pool.device, rows.shape[0]
-    _check_tensor("pool", pool, torch.uint8, (None, KV4_ROW_BYTES), dev)
+    dev, n = pool.get_device(), rows.shape[0]
+    _check_tensor("pool", pool, torch.uint8, (pool.shape[0], KV4_ROW_BYTES), dev)
     _check_tensor("slot_map", slot_map, torch.int32, (n,), dev)
-    if rows.dtype != torch.bfloat16 or rows.device != dev or rows.dim() != 2 or rows.shape[1] != D_LATENT + D_ROPE:
-        raise ValueError(f"rows must be bf16 [n, 576] on {dev}: got {rows.dtype} {tuple(rows.shape)} on {rows.device}")
+    if rows.dtype is not torch.bfloat16 or rows.get_device() != dev or rows.shape != (n, D_LATENT + D_ROPE):
+        raise ValueError(f"rows must be bf16 [n, 576] on cuda:{dev}: got {rows.dtype} {tuple(rows.shape)} on {rows.device}")
     if rows.stride(1) != 1:
         raise ValueError("the dims of a row must be contiguous")
     if dev_status is not None:
         _check_tensor("dev_status", dev_status, torch.int32, (1,), dev)
-    s, here = _on(dev, stream)
+    raw, here = _on(dev, stream)
     with here:
         rc = load_library().mla_kv4_append(pool.data_ptr(), pool.shape[0], rows.data_ptr(),
                                            rows.stride(0) if n > 1 else D_LATENT + D_ROPE, slot_map.data_ptr(), n,
-                                           int(debug), _ptr_or_none(dev_status), s.cuda_stream)
+                                           int(debug), _ptr_or_none(dev_status), raw)
     _check(rc, "mla_kv4_append")
     return pool
 
@@ -387,19 +404,19 @@ def kv4_append(pool, rows, slot_map, *, debug: bool = False, dev_status=None, st
 def kv4_gather(pool, slots, *, out=None, debug: bool = False, dev_status=None, stream=None):
     """Rows of the 4-bit pool as bf16 [n, 576], exactly; slot -1 gives zeros (``include/mla_kv4.h``)."""
     import torch
-    dev, n = pool.device, slots.shape[0]
-    _check_tensor("pool", pool, torch.uint8, (None, KV4_ROW_BYTES), dev)
+    dev, n = pool.get_device(), slots.shape[0]
+    _check_tensor("pool", pool, torch.uint8, (pool.shape[0], KV4_ROW_BYTES), dev)
     _check_tensor("slots", slots, torch.int32, (n,), dev)
     if dev_status is not None:
         _check_tensor("dev_status", dev_status, torch.int32, (1,), dev)
-    s, here = _on(dev, stream)
+    raw, here = _on(dev, stream)
     with here:
         if out is None:
-            out = torch.empty((n, D_LATENT + D_ROPE), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((n, D_LATENT + D_ROPE), dtype=torch.bfloat16, device=pool.device)
         else:
             _check_tensor("out", out, torch.bfloat16, (n, D_LATENT + D_ROPE), dev)
         rc = load_library().mla_kv4_gather(pool.data_ptr(), pool.shape[0], slots.data_ptr(), n, out.data_ptr(),
-                                           int(debug), _ptr_or_none(dev_status), s.cuda_stream)
+                                           int(debug), _ptr_or_none(dev_status), raw)
     _check(rc, "mla_kv4_gather")
     return out
 
@@ -437,39 +454,40 @@ def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, 
     tree_sizes: int32 [B] or None. Returns (out [B*T, H, 512], lse [B*T, H]).
     """
     import torch
-    dev, i32 = q.device, torch.int32
+    dev, i32 = q.get_device(), torch.int32
     B, T = tree_parent.shape
     H = q.shape[1]
     out_type = torch.bfloat16 if out_dtype == MLA_DTYPE_BF16 else torch.float32
     _check_tensor("q", q, torch.bfloat16, (B * T, H, D_LATENT + D_ROPE), dev)
-    _check_tensor("pool", pool, torch.uint8, (None, KV4_ROW_BYTES), dev)
-    _check_tensor("slot_table", slot_table, i32, (B, None), dev)
+    slots, stride = pool.shape[0], slot_table.shape[-1]
+    _check_tensor("pool", pool, torch.uint8, (slots, KV4_ROW_BYTES), dev)
+    _check_tensor("slot_table", slot_table, i32, (B, stride), dev)
     _check_tensor("seq_lens", seq_lens, i32, (B,), dev)
     _check_tensor("tree_parent", tree_parent, i32, (B, T), dev)
     if tree_sizes is not None:
         _check_tensor("tree_sizes", tree_sizes, i32, (B,), dev)
     if dev_status is not None:
         _check_tensor("dev_status", dev_status, i32, (1,), dev)
-    s, here = _on(dev, stream)
+    raw, here = _on(dev, stream)
     with here:
-        desc, need = _kv4_desc(dev.index, B, T, H, pool.shape[0], slot_table.shape[1], max_seq_len, softmax_scale,
+        desc, need = _kv4_desc(dev, B, T, H, slots, stride, max_seq_len, softmax_scale,
                                out_dtype, DEFAULT_FLAGS if flags is None else flags, num_splits, total_tokens_hint)
         if out is None:
-            out = torch.empty((B * T, H, D_LATENT), device=dev, dtype=out_type)
+            out = torch.empty((B * T, H, D_LATENT), device=q.device, dtype=out_type)
         else:
             _check_tensor("out", out, out_type, (B * T, H, D_LATENT), dev)
         if lse is None:
-            lse = torch.empty((B * T, H), device=dev, dtype=torch.float32)
+            lse = torch.empty((B * T, H), device=q.device, dtype=torch.float32)
         else:
             _check_tensor("lse", lse, torch.float32, (B * T, H), dev)
         if workspace is None:
-            workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
         else:
-            _check_tensor("workspace", workspace, torch.uint8, (None,), dev)
+            _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
         rc = load_library().mla_verify_attn_kv4(
             ctypes.byref(desc), q.data_ptr(), pool.data_ptr(), slot_table.data_ptr(), seq_lens.data_ptr(),
             _ptr_or_none(tree_sizes), tree_parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-            workspace.numel(), _ptr_or_none(dev_status), s.cuda_stream)
+            workspace.numel(), _ptr_or_none(dev_status), raw)
     _check(rc, "mla_verify_attn_kv4")
     return out, lse
 

@@ -3,6 +3,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace mla {
@@ -102,11 +104,16 @@ extern "C" int mla_verify_plan(const mla_verify_desc* d, int32_t num_sms, mla_ve
 
 namespace mla {
 int current_sms(int32_t* sms) {
+  // A device's SM count, looked up once (a racing second lookup stores the same number).
+  static std::atomic<int32_t> known[64];
   int dev = 0, n = 0, major = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_NO_DEVICE;
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return MLA_OK;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return MLA_ERR_NO_DEVICE;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return MLA_ERR_NO_DEVICE;
   if (major != 10) return MLA_ERR_NO_DEVICE;
+  if (cached) known[dev].store(n, std::memory_order_relaxed);
   *sms = n;
   return MLA_OK;
 }

@@ -50,13 +50,14 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
     tiles = cdiv(cdiv(total, tile) * p.row_tiles, slots);
   } else {
     // The chunk that minimises the estimated makespan: waves of units x (its tiles + a fixed cost of
-    // kUnitTiles for the set-up, the pipeline's fill and the write-back), plus the combine's reading.
+    // kUnitTiles for the set-up, the pipeline's fill and the write-back), plus the combine's reading. More
+    // than four units a slot never pay, so the splits to look at are few.
     double best = 1e300;
-    for (int64_t ct = 1; ct <= max_tiles; ++ct) {
-      const int64_t splits = cdiv(max_tiles, ct);
-      if (splits > kMaxSplits) continue;
-      const int64_t units = total < uniform ? p.row_tiles * (cdiv(total, ct * tile) + d->num_seqs / 2)
-                                            : (int64_t)d->num_seqs * p.row_tiles * splits;
+    const int64_t per_split = (int64_t)d->num_seqs * p.row_tiles;
+    const int64_t most = cdiv(4 * slots, per_split) < max_tiles ? cdiv(4 * slots, per_split) : max_tiles;
+    for (int64_t want = most; want >= 1; --want) {
+      const int64_t ct = cdiv(max_tiles, want), splits = cdiv(max_tiles, ct);
+      const int64_t units = total < uniform ? p.row_tiles * (cdiv(total, ct * tile) + d->num_seqs / 2) : per_split * splits;
       const double cost = (double)cdiv(units, slots) * (double)(ct + kUnitTiles) +
                           0.25 * (double)splits * p.row_tiles * d->num_seqs / slots;
       if (cost < best - 1e-9) {
