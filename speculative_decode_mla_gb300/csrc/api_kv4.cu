@@ -9,7 +9,6 @@ namespace {
 constexpr int kTcRowsPerTile = 128;  // query rows of a pair of CTAs
 constexpr int kSimtRowsPerTile = 8;  // one warp per row, 8 warps per CTA
 constexpr int kMaxSplits = 65535;
-constexpr int kUnitTiles = 4;        // a unit's fixed cost in tiles of 128 positions
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -40,39 +39,21 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   const int64_t max_tiles = cdiv(max_n, tile);
   const int64_t uniform = (int64_t)d->num_seqs * max_n;
   const int64_t total = d->total_tokens_hint > 0 && d->total_tokens_hint < uniform ? d->total_tokens_hint : uniform;
-  // Work units are (sequence, row tile, chunk): one pair of SMs each, or small CTAs, several per SM.
+  const int64_t row_tiles = (int64_t)d->num_seqs * p.row_tiles;
+  if ((max_tiles + kKv4SegmentUnits) * row_tiles > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
+  // SIMT: units of (sequence, row tile, chunk), small CTAs, several per SM. tcgen05: one cluster per pair of SMs; the
+  // clusters share all tiles equally, at least chunk_tokens / 128 each. That least share only bounds the number of
+  // splits that the workspace has room for: the kernel takes the even share of the lengths that it finds.
   const int64_t slots = simt ? (int64_t)num_sms * 8 : (num_sms / 2 > 0 ? num_sms / 2 : 1);
-  int64_t tiles = 1;
-  if (d->num_splits > 0) {
-    tiles = cdiv(max_tiles, d->num_splits);
-  } else if (simt || (total < uniform && d->num_seqs <= kLptMaxSeqs)) {
-    // a batch of different lengths, longest units first: the slots' even share of all tiles
-    tiles = cdiv(cdiv(total, tile) * p.row_tiles, slots);
-  } else {
-    // The chunk that minimises the estimated makespan: waves of units x (its tiles + a fixed cost of
-    // kUnitTiles for the set-up, the pipeline's fill and the write-back), plus the combine's reading. More
-    // than four units a slot never pay, so the splits to look at are few.
-    double best = 1e300;
-    const int64_t per_split = (int64_t)d->num_seqs * p.row_tiles;
-    const int64_t most = cdiv(4 * slots, per_split) < max_tiles ? cdiv(4 * slots, per_split) : max_tiles;
-    for (int64_t want = most; want >= 1; --want) {
-      const int64_t ct = cdiv(max_tiles, want), splits = cdiv(max_tiles, ct);
-      const int64_t units = total < uniform ? p.row_tiles * (cdiv(total, ct * tile) + d->num_seqs / 2) : per_split * splits;
-      const double cost = (double)cdiv(units, slots) * (double)(ct + kUnitTiles) +
-                          0.25 * (double)splits * p.row_tiles * d->num_seqs / slots;
-      if (cost < best - 1e-9) {
-        best = cost;
-        tiles = ct;
-      }
-    }
-  }
+  int64_t tiles = d->num_splits > 0 ? cdiv(max_tiles, d->num_splits) : cdiv(cdiv(total, tile) * p.row_tiles, slots);
   tiles = tiles < 1 ? 1 : tiles > max_tiles ? max_tiles : tiles;
-  if (cdiv(max_tiles, tiles) > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits);
+  if (cdiv(max_tiles, tiles) + 1 > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits - 1);
   p.chunk_tokens = (int32_t)(tiles * tile);
-  p.num_splits = (int32_t)cdiv(max_n, p.chunk_tokens);
-  const int64_t units = (int64_t)d->num_seqs * p.row_tiles * p.num_splits;
-  if (units > 0x3fffffff) return MLA_ERR_UNSUPPORTED;
-  p.ctas = (int32_t)(simt ? units : 2 * units);
+  if (simt || row_tiles == 1) p.num_splits = (int32_t)cdiv(max_tiles, tiles);
+  else p.num_splits = (int32_t)((max_tiles + tiles - 2) / tiles + 1);  // a row tile may begin inside a share
+  if (simt && row_tiles * p.num_splits > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
+  const int64_t all = row_tiles * (max_tiles + kKv4SegmentUnits) - kKv4SegmentUnits;
+  p.ctas = (int32_t)(simt ? row_tiles * p.num_splits : 2 * (all < slots ? all : slots));
   const int64_t rows = (int64_t)d->num_seqs * R;
   p.workspace_bytes = part_o_bytes(p, rows) + cdiv((int64_t)p.num_splits * rows * 4, 256) * 256;
   *plan = p;
@@ -136,14 +117,13 @@ extern "C" int mla_verify_attn_kv4(const mla_verify_desc* d, const void* q, cons
   a.splits = p.num_splits;
   a.row_tiles = p.row_tiles;
   a.rows_per_tile = p.rows_per_tile;
-  a.lpt = (p.kernel == 0 && d->num_seqs >= 2 && d->num_seqs <= kLptMaxSeqs) ? 1 : 0;
   a.debug = debug ? 1 : 0;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
-  if ((p.kernel == 1 ? launch_verify_kv4_simt(a, s) : launch_verify_kv4_tc(a, s)) != cudaSuccess) return MLA_ERR_CUDA;
+  if ((p.kernel == 1 ? launch_verify_kv4_simt(a, s) : launch_verify_kv4_tc(a, p.ctas, s)) != cudaSuccess) return MLA_ERR_CUDA;
   if (launch_combine(p.num_splits, a.rows, kDLatent, a.part_o, MLA_DTYPE_F16, a.part_lse, out, lse, d->out_dtype,
                      /*dependent=*/true, s) != cudaSuccess)
     return MLA_ERR_CUDA;

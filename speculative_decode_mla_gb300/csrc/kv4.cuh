@@ -13,7 +13,10 @@ constexpr int kKv4Rope = kKv4Codes + kKv4Scales;           // the RoPE dims star
 constexpr int kKv4Row = kKv4Rope + 2 * kDRope;             // 416 bytes
 static_assert(kKv4Row == MLA_KV4_ROW_BYTES && kKv4Row % 16 == 0, "row format");
 
-constexpr int kKv4TileTokens = 128;                        // positions per tile of the tcgen05 kernel
+constexpr int kKv4TileTokens = 128;  // positions per tile of the tcgen05 kernel
+// What starting and ending a run of tiles costs, in tiles. At 0, 1, 2, 3, 4 a batch of 32 sequences took 118, 116, 111,
+// 114, 114 us, one of 61 took 119, 104, 101, 104, 106 (in the state of the kernel in which this was compared).
+constexpr int kKv4SegmentUnits = 2;
 
 // The two values of a code byte (dim 2i low, dim 2i+1 high) as packed fp16, exact.
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {

@@ -372,6 +372,42 @@ def test_verify_ragged_trees_and_hints(hint):
     assert pad.any() and (got[0][pad] == 0).all()
 
 
+MANY = [int(x) for x in np.random.default_rng(5).integers(0, 900, size=100)]
+
+
+@pytest.mark.parametrize("lens,T,H,kw", [
+    (MANY, 2, 3, {}), (MANY, 2, 3, dict(num_splits=1)), (MANY, 2, 3, dict(num_splits=3, total_tokens_hint=1)),
+    ([900, 0, 3000, 1500], 16, 20, {}), ([900, 0, 3000, 1500], 16, 20, dict(num_splits=1)),
+    ([900, 0, 3000, 1500], 16, 20, dict(num_splits=2)), ([900, 0, 3000, 1500], 16, 20, dict(total_tokens_hint=10 ** 9)),
+    ([5] * 33 + [6000], 5, 29, {}), ([5] * 33 + [6000], 5, 29, dict(num_splits=1)), ([0] * 70, 1, 1, {}),
+    ([200, 1] * 80, 1, 2, dict(total_tokens_hint=300)),
+], ids=lambda x: str(len(x)) if isinstance(x, list) else None)
+def test_verify_shares_that_begin_inside_a_sequence(lens, T, H, kw):
+    """A pair of CTAs takes a run of tiles that may hold several sequences and row tiles, whole or in part."""
+    p, rows, bits = problem(lens, T, H, 500 + len(lens))
+    assert_close(call(p, rows, **kw), expect(p, bits), p.q, bits)
+    sizes = 1 + np.arange(p.B) % T
+    assert_close(call(p, rows, sizes=sizes, **kw), expect(p, bits, sizes=sizes), p.q, bits)
+
+
+def test_debug_checks_of_the_last_sequences():
+    """Bad slots and parents that only a cluster's later sequences hold are reported too."""
+    import torch
+    import speculative_decode_mla_gb300 as m
+    p, rows, bits = problem(MANY, 2, 3, 51)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(flags=m.MLA_FLAG_DEBUG_CHECKS, dev_status=st, num_splits=1)
+    assert_close(call(p, rows, **kw), expect(p, bits), p.q, bits)
+    for b in (1, 50, 99):
+        table, parents = p.slot_table.copy(), p.tree_parent.copy()
+        table[b, p.seq_lens[b]] = -1
+        parents[b, 1] = 1
+        for bad, flag in ((dict(table=table), m.CHECK_BAD_SLOT), (dict(parents=parents), m.CHECK_BAD_PARENT)):
+            with pytest.raises(m.MLAError):
+                call(p, rows, **kw, **bad)
+            assert st.item() == flag
+
+
 @pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -20, 2.0 ** -6, 1.0, 8.0])
 def test_verify_queries_of_any_size(size):
     """Rows of very different sizes in one tile, up to scores that let one key take all the weight."""
