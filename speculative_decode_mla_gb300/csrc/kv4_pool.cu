@@ -26,33 +26,42 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 // The e4m3 scale of a block: max|x| / 6, the exact quotient rounded to nearest even and at most
 // 448; NaN (0x7f) when the block holds a NaN or an infinity. `top`: the largest bf16 magnitude as bits.
-// The fp32 quotient is not on a midpoint of e4m3 unless the exact one is (top has 8 significant
-// bits, a midpoint times 6 has 7), so rounding twice is harmless.
+// top times fp32's 1/6 serves as the quotient: fp32's 1/6 is off by 2^-25 of itself. If top / 6 is a midpoint m of e4m3
+// (at most 5 significant bits), the product lies within m * 2^-25 of m, under half an ulp, and rounds to m; if not, it
+// is off every midpoint by 2^-8 of its size (top has 8 significant bits, 6 m has 7), so rounding twice is harmless.
 __device__ __forceinline__ uint32_t block_scale(uint32_t top) {
-  if (top >= 0x7f80u) return 0x7fu;
   uint16_t s;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(__fdiv_rn(__uint_as_float(top << 16), 6.f)));
-  return s & 0xffu;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(__uint_as_float(top << 16) * (1.f / 6.f)));
+  return top >= 0x7f80u ? 0x7fu : s & 0xffu;
 }
 
-// Codes of eight values (four words of bf16 pairs) under the scale byte. y = x / s is taken as
-// x * (1/s) and rounded to a multiple of 2^-11 by adding and taking away 1.5 * 2^12: a quotient on one
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+// Codes of eight values (four words of bf16 pairs) under the scale byte. y = x / s is taken as x * r, r = 1 / s within
+// 2^-23 of itself, and rounded to a multiple of 2^-11 by adding and taking away 1.5 * 2^12: a quotient on one
 // of e2m1's midpoints (0.25 .. 5) comes out exactly on it, and any other stays off it, since x has 8
 // significant bits and s * midpoint at most 7, so they differ by 2^-8 of their size or not at all.
 __device__ __forceinline__ uint32_t block_codes(const uint4& w, uint32_t scale) {
   const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(scale) & 0xffffu)));
-  const float r = (s > 0.f) ? __frcp_rn(s) : 0.f;  // scale 0 or NaN: codes 0
-  const float magic = 6144.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // (s is 0, NaN or a normal fp32 number)
+  const uint64_t rr = pack2(r, r), magic = pack2(6144.f, 6144.f), minus = pack2(-6144.f, -6144.f);
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  uint32_t out = 0;
+  uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = fmaf(bf16_lo(x[i]), r, magic) - magic, b = fmaf(bf16_hi(x[i]), r, magic) - magic;
-    uint32_t c;
-    asm("{\n.reg .b8 d;\ncvt.rn.satfinite.e2m1x2.f32 d, %1, %2;\nmov.b32 %0, {d, 0, 0, 0};\n}" : "=r"(c) : "f"(b), "f"(a));
-    out |= c << (8 * i);
+    const uint64_t v = pack2(bf16_lo(x[i]), bf16_hi(x[i]));
+    asm("{\n.reg .b64 y;\n.reg .f32 lo, hi;\n.reg .b8 d;\n"
+        "fma.rn.f32x2 y, %1, %2, %3;\nadd.rn.f32x2 y, y, %4;\nmov.b64 {lo, hi}, y;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 d, hi, lo;\nmov.b32 %0, {d, 0, 0, 0};\n}"
+        : "=r"(c[i])
+        : "l"(v), "l"(rr), "l"(magic), "l"(minus));
   }
-  return s > 0.f ? out : 0u;  // (0 * infinity is no code)
+  const uint32_t out = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  return s > 0.f ? out : 0u;  // (scale 0 or NaN: codes 0)
 }
 
 __device__ __forceinline__ uint32_t top_of(const uint4& w) {
