@@ -28,9 +28,14 @@ struct MapArgs {
   int32_t B, page_size, num_pages, free_capacity, block_stride, slot_stride, debug;
 };
 
-// What sequence b asks for: n new tokens from position L on, h positions held, `take` pages.
+// Pages of x >= 0 positions (32-bit division: a 64-bit one takes several times as long, and there are few warps to hide it).
+__device__ __forceinline__ int32_t pages_of(int32_t x, int32_t page_size) {
+  return x == 0 ? 0 : (int32_t)((uint32_t)(x - 1) / (uint32_t)page_size) + 1;
+}
+
+// What sequence b asks for: n new tokens from position L on, h positions held in `have` pages, `take` pages more.
 struct Wish {
-  int32_t L, h, n, take, end;
+  int32_t L, h, n, have, take, end;
   bool ok;
 };
 __device__ __forceinline__ Wish wish_of(const MapArgs& a, int b) {
@@ -39,16 +44,19 @@ __device__ __forceinline__ Wish wish_of(const MapArgs& a, int b) {
   w.n = a.new_lens[b];
   w.h = a.held_lens ? a.held_lens[b] : w.L;
   const int64_t end = max((int64_t)w.h, (int64_t)w.L + w.n);
-  const int64_t p = a.page_size;
-  w.ok = w.L >= 0 && w.n >= 0 && w.h >= w.L && end <= a.slot_stride &&
-         (!a.block_table || (end + p - 1) / p <= a.block_stride);
-  if (!w.ok) {
-    w.n = w.take = 0;
-    w.end = w.h;
-    return w;
+  w.ok = w.L >= 0 && w.n >= 0 && w.h >= w.L && end <= a.slot_stride;
+  w.have = w.take = 0;
+  w.end = w.h;
+  if (w.ok) {
+    const int32_t pages = pages_of((int32_t)end, a.page_size);
+    w.ok = !a.block_table || pages <= a.block_stride;
+    if (w.ok) {
+      w.have = pages_of(w.h, a.page_size);
+      w.take = pages - w.have;
+      w.end = (int32_t)end;
+    }
   }
-  w.end = (int32_t)end;
-  w.take = (int32_t)((end + p - 1) / p - ((int64_t)w.h + p - 1) / p);
+  if (!w.ok) w.n = 0;
   return w;
 }
 
@@ -77,8 +85,9 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs a) 
   const int b0 = tid * per, b1 = min(a.B, b0 + per);
   const int32_t fc = *a.free_count;
   longlong2 own = {0, 0};
+  Wish w = {};  // (of the last one; with one sequence a thread, the only one)
   for (int b = b0; b < b1; ++b) {
-    const Wish w = wish_of(a, b);
+    w = wish_of(a, b);
     if (!w.ok && first_cta) report(a.dev_status, a.debug, MLA_CHECK_BAD_LENGTH);
     own.x += w.n;
     own.y += w.take;
@@ -99,7 +108,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs a) 
   const bool granted = total.x <= a.map_capacity && fc >= 0 && fc <= a.free_capacity && total.y <= fc;
   long long cu = base.x + inc.x - own.x, pages = base.y + inc.y - own.y;
   for (int b = b0; b < b1; ++b) {
-    const Wish w = wish_of(a, b);
+    if (per > 1) w = wish_of(a, b);
     s_cu[b] = granted ? (int32_t)cu : 0;
     s_first[b] = granted ? (int32_t)pages : 0;
     if (first_cta) {
@@ -126,8 +135,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs a) 
   for (int64_t i0 = ((int64_t)blockIdx.x * kMapThreads + tid) * kMapTokens; i0 < a.map_capacity; i0 += step) {
     int32_t out[kMapTokens];
     int b = -1;
-    Wish w = {};
-    int32_t have = 0, next = 0;
+    int32_t next = 0;
 #pragma unroll
     for (int k = 0; k < kMapTokens; ++k) {
       const int64_t i = i0 + k;
@@ -143,7 +151,6 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs a) 
         b = lo;
         next = s_cu[b + 1];
         w = wish_of(a, b);
-        have = (int32_t)(((int64_t)w.h + a.page_size - 1) / a.page_size);
       }
       const int32_t t = w.L + (int32_t)(i - s_cu[b]);
       int32_t* place = a.slot_table + (int64_t)b * a.slot_stride + t;
@@ -155,10 +162,10 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs a) 
           slot = -1;
         }
       } else {
-        const int32_t k_page = t / a.page_size, in_page = t - k_page * a.page_size;
+        const int32_t k_page = (int32_t)((uint32_t)t / (uint32_t)a.page_size), in_page = t - k_page * a.page_size;
         int32_t page;
-        if (k_page >= have) {
-          page = a.free_pages[fc - 1 - (s_first[b] + (k_page - have))];
+        if (k_page >= w.have) {
+          page = a.free_pages[fc - 1 - (s_first[b] + (k_page - w.have))];
           if (in_page == 0 && a.block_table) a.block_table[(int64_t)b * a.block_stride + k_page] = page;
         } else {
           page = a.block_table[(int64_t)b * a.block_stride + k_page];
