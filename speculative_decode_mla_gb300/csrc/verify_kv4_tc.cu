@@ -38,13 +38,14 @@
 // TMEM (512 columns): O [0, 256), two S buffers [256, 384), Q's dims 0..255 [384, 512) (both lane halves hold the
 // CTA's 64 rows); Q's dims 256..511 and RoPE dims are in shared memory.
 //
-// What bounds it: shared memory. Per tile and SM, at 128 bytes a cycle: 152 KB of K, V, RoPE dims and P written, 176 KB
-// of operands read by S (72 of K, 40 of Q) and PV (64 of V; P twice, 32), the gathered rows through the same L1 (40 KB):
-// about 2900 cycles, while the tensor cores need 2200 (64 rows of each SM are half their rate) and the tile takes
-// about 3500. A segment costs about two tiles more, the launch and the merge about 10 us. At 72 registers the gather
-// does not spill; at 64 with 24 bytes spilled the 131072-position case below took 918 us instead of 867.
-//   rows x positions (sequences): 64 x 1 Ki 13.2 us, 128 x 64 Ki 27.7, 256 x 180 Ki 95, 128 x 301 k (32) 95,
-//   64 x 250 k (61) 87, 4096 x 128 Ki 867 (1348 TFLOP/s); merge included
+// What bounds it: the L1 data path. Per tile and SM its counters show (256 rows x 180 Ki positions) 2780 wavefronts of
+// loads and stores (152 KB of K, V, RoPE dims and P stored: 1220 at least, 1440 with the barriers; the gathered rows,
+// 40 KB, in and out to registers: 1120) and 1660 of MMA operands (S: 72 KB of K, 40 of Q; PV: 64 of V, P twice), together
+// 97% of the SM's active cycles; a tile takes about 4050, the tensor cores need 2200 of them (64 rows on each SM are half
+// their rate). A segment costs about two tiles more, launch and merge about 10 us. The gather does not spill at 72
+// registers; at 64, with 24 bytes spilled, 4096 rows x 128 Ki took 918 us instead of 867.
+//   rows x positions (sequences): 64 x 1 Ki 12.9 us, 128 x 64 Ki 27.5, 256 x 180 Ki 95, 128 x 301 k (32) 95,
+//   64 x 250 k (61) 87, 4096 x 128 Ki 870 (1.34 PFLOP/s); merge included
 // One unit (sequence, row tile, chunk) a cluster, without the shares: 12.7, 28.5, 95, 118, 105, 938.
 //
 // Positions past a sequence's end read slot 0's row and are masked; values whose scale is NaN are 0
