@@ -40,7 +40,8 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   const int64_t uniform = (int64_t)d->num_seqs * max_n;
   const int64_t total = d->total_tokens_hint > 0 && d->total_tokens_hint < uniform ? d->total_tokens_hint : uniform;
   const int64_t row_tiles = (int64_t)d->num_seqs * p.row_tiles;
-  if ((max_tiles + kKv4SegmentUnits) * row_tiles > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
+  // (the kernels count tiles, and positions of a segment, in 32 bits)
+  if (max_n > 0x7fffff00 || (max_tiles + kKv4SegmentUnits) * row_tiles > 0x3fffffff) return MLA_ERR_UNSUPPORTED;
   // SIMT: units of (sequence, row tile, chunk), small CTAs, several per SM. tcgen05: one cluster per pair of SMs; the
   // clusters share all tiles equally, at least chunk_tokens / 128 each. That least share only bounds the number of
   // splits that the workspace has room for: the kernel takes the even share of the lengths that it finds.

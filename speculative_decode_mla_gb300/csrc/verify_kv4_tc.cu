@@ -42,10 +42,11 @@
 // loads and stores (152 KB of K, V, RoPE dims and P stored: 1220 at least, 1440 with the barriers; the gathered rows,
 // 40 KB, in and out to registers: 1120) and 1660 of MMA operands (S: 72 KB of K, 40 of Q; PV: 64 of V, P twice), together
 // 97% of the SM's active cycles; a tile takes about 4050, the tensor cores need 2200 of them (64 rows on each SM are half
-// their rate). A segment costs about two tiles more, launch and merge about 10 us. The gather does not spill at 72
+// their rate). A segment costs about three tiles more (O out, Q in, and the
+// first tile's K and V before the first PV), launch and merge about 10 us. The gather does not spill at 72
 // registers; at 64, with 24 bytes spilled, 4096 rows x 128 Ki took 918 us instead of 867.
-//   rows x positions (sequences): 64 x 1 Ki 12.9 us, 128 x 64 Ki 27.5, 256 x 180 Ki 95, 128 x 301 k (32) 95,
-//   64 x 250 k (61) 87, 4096 x 128 Ki 870 (1.34 PFLOP/s); merge included
+//   rows x positions (sequences): 64 x 1 Ki 13.4 us, 128 x 64 Ki 27.7, 256 x 180 Ki 95, 128 x 301 k (32) 95,
+//   64 x 250 k (61) 87, 4096 x 128 Ki 867 (1.35 PFLOP/s); merge included
 // One unit (sequence, row tile, chunk) a cluster, without the shares: 12.7, 28.5, 95, 118, 105, 938.
 //
 // Positions past a sequence's end read slot 0's row and are masked; values whose scale is NaN are 0
@@ -94,6 +95,7 @@ constexpr int kQTmemDims = 256;
 static_assert(2 * kVHalfBytes >= kCtaRows * kQTmemDims * 2, "half of Q passes through V's place");
 constexpr int kOutRow = kDLatent * 2 + 16;  // a row of the output on its way out: 8 rows' chunks lie in different banks
 static_assert(kCtaRows * kOutRow <= kKSlots * kKSlotBytes, "output rows");
+constexpr int kPrefetchTiles = 3;  // of the next segment, to L2: 4096 sequences of 300 positions took 911 us with 1, 878 with 3
 constexpr float kPBias = 7.f;
 
 constexpr int kBarKFull = 0, kBarKEmpty = kKSlots, kBarVFull = 2 * kKSlots /*2*/, kBarVEmpty = kBarVFull + 2 /*2*/,
@@ -259,15 +261,13 @@ struct Segment {
   int32_t L, Tb;
 };
 // The segment that begins at unit w, for a cluster whose share ends at w_end; w goes to the next row tile first where
-// it lies behind the last tile of one (warp-collective).
-__device__ __forceinline__ Segment segment_at(const VerifyArgs& a, int lane, const Lengths& head, int& w, int w_end,
+// it lies behind the last tile of one. The search begins at the 32 sequences from b0 on, with `base` units before them and
+// the lengths x, and leaves the place where it ended (warp-collective).
+__device__ __forceinline__ Segment segment_at(const VerifyArgs& a, int lane, Lengths x, int& b0, int& base, int& w, int w_end,
                                               int share) {
   Segment g = {};
-  Lengths x = head;
-  int base = 0;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    if (b0 > 0) x = lengths_from(a, lane, b0);
+  while (b0 < a.B) {
     const int own = units_of(a, x.ntiles);
     int inc = own;
 #pragma unroll
@@ -295,13 +295,15 @@ __device__ __forceinline__ Segment segment_at(const VerifyArgs& a, int lane, con
       return g;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
+    b0 += 32;
+    x = lengths_from(a, lane, b0);
   }
   return g;
 }
 
 // The segments of a cluster, one after the other (every lane of the warp calls these).
 struct Walk {
-  int share, w, w_end;
+  int share, w, w_end, b0 = 0, base = 0;
   __device__ __forceinline__ Walk(const VerifyArgs& a, int lane, const Lengths& head) {
     const int clusters = (int)(gridDim.x >> 1), total = all_units(a, lane, head);
     share = max(a.chunk / kKeys, (total + clusters - 1) / clusters);
@@ -310,7 +312,7 @@ struct Walk {
   }
   // The next one, if w < w_end says that the share goes on; no tiles: there is none.
   __device__ __forceinline__ Segment next(const VerifyArgs& a, int lane, const Lengths& head) {
-    Segment g = segment_at(a, lane, head, w, w_end, share);
+    Segment g = segment_at(a, lane, head, b0, base, w, w_end, share);
     if (w >= w_end) g.ntiles = 0;
     w += g.ntiles + kKv4SegmentUnits;
     return g;
@@ -321,7 +323,10 @@ __device__ __forceinline__ Segment segment_number(const VerifyArgs& a, int lane,
   const Lengths head = lengths_from(a, lane, 0);
   Walk walk(a, lane, head);
   Segment g = {};
-  for (int i = 0; i <= n; ++i) g = walk.next(a, lane, head);
+  for (int i = 0; i <= n; ++i) {
+    walk.b0 = walk.base = 0;
+    g = walk.next(a, lane, head);
+  }
   more = walk.w < walk.w_end;
   return g;
 }
@@ -762,25 +767,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
     }
     if (warp == kSegWarp) {
       // ------------------------------------------------------------ the segments to come, and their first data to L2
+      // This CTA's rows of Q, and its keys of the first tiles: later ones are loaded a tile ahead, which hides the latency.
+      auto prefetch = [&](const Segment& sg) {
+        const int row0 = sg.row_tile * kRows + (int)rank * kCtaRows;
+        const int rows_here = min(kCtaRows, min(R, sg.Tb * a.H) - row0);
+        if (lane == 0 && rows_here > 0) prefetch_l2(a.q + ((int64_t)sg.b * R + row0) * kDK, rows_here * kDK * 2);
+        const int32_t* tab = a.slot_table + (int64_t)sg.b * a.stride;
+        const int64_t first = (int64_t)sg.tile0 * kKeys + (int)rank * kOwn + lane, end = (int64_t)sg.L + sg.Tb;
+#pragma unroll 1
+        for (int t = 0; t < min(sg.ntiles, kPrefetchTiles); ++t)
+#pragma unroll
+          for (int i = 0; i < kOwn; i += 32) {
+            const int64_t at = first + t * kKeys + i;
+            const int32_t slot = at < end ? tab[at] : -1;
+            if (slot >= 0 && slot < a.num_slots)
+              prefetch_l2(reinterpret_cast<const uint8_t*>(a.kv) + (int64_t)slot * kKv4Row, kKv4Row);
+          }
+        __syncwarp();
+      };
       for (int n = 1; walk.w < walk.w_end; ++n) {
         // the place of segment n - 2 is free once Q of segment n - 1 is in place: every role has read that one
         if (!wait_warp(bar(kBarQFull), (n - 1) & 1, abort_flag)) break;
-        const Segment sg = walk.next(a, lane, lengths_from(a, lane, 0));
+        const Segment sg = walk.next(a, lane, lengths_from(a, lane, walk.b0));
         if (lane == 0) {
           put_segment(n, sg, walk.w < walk.w_end);
           mbar_arrive(bar(kBarSeg + (n & 1)));
         }
         __syncwarp();
-        const int row0 = sg.row_tile * kRows + (int)rank * kCtaRows;
-        const int rows_here = min(kCtaRows, min(R, sg.Tb * a.H) - row0);
-        if (lane == 0 && rows_here > 0) prefetch_l2(a.q + ((int64_t)sg.b * R + row0) * kDK, rows_here * kDK * 2);
-        const int64_t at = (int64_t)sg.tile0 * kKeys + (int)rank * kOwn + lane;
-        for (int i = 0; i < kOwn; i += 32) {
-          if (at + i >= (int64_t)sg.L + sg.Tb) break;
-          const int32_t slot = a.slot_table[(int64_t)sg.b * a.stride + at + i];
-          if (slot >= 0 && slot < a.num_slots) prefetch_l2(reinterpret_cast<const uint8_t*>(a.kv) + (int64_t)slot * kKv4Row, kKv4Row);
-        }
-        __syncwarp();
+        prefetch(sg);
       }
     }
     if (rank == 0 && warp <= kPVWarp) {  // drain: every MMA that the elected thread issued has completed once this flips

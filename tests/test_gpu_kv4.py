@@ -390,6 +390,19 @@ def test_verify_shares_that_begin_inside_a_sequence(lens, T, H, kw):
     assert_close(call(p, rows, sizes=sizes, **kw), expect(p, bits, sizes=sizes), p.q, bits)
 
 
+@pytest.mark.parametrize("B,T", [(33, 1), (64, 2), (65, 1), (1000, 1), (3000, 2)])
+def test_verify_many_short_sequences(B, T):
+    """More sequences than a warp has lanes, most of them one tile: both kernels over the same rows."""
+    import speculative_decode_mla_gb300 as m
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in np.where(rng.random(B) < 0.8, rng.integers(0, 100, B), rng.integers(100, 700, B))]
+    p, rows, bits = problem(lens, T, 3, 600 + B)
+    got, ref = call(p, rows, out_dtype=m.MLA_DTYPE_F32), call(p, rows, out_dtype=m.MLA_DTYPE_F32, flags=m.MLA_FLAG_SIMT)
+    assert_close(got, ref, p.q, bits, f32=True)
+    if B <= 65:
+        assert_close(got, expect(p, bits), p.q, bits, f32=True)
+
+
 def test_debug_checks_of_the_last_sequences():
     """Bad slots and parents that only a cluster's later sequences hold are reported too."""
     import torch

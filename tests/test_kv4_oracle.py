@@ -155,7 +155,8 @@ def test_verify_kv4_refuses(lib):
 @pytest.mark.parametrize("bad", [dict(num_nodes=0), dict(num_nodes=65), dict(num_heads=0), dict(num_seqs=0),
                                  dict(slot_table_stride=100), dict(num_slots=0), dict(max_seq_len=-1),
                                  dict(softmax_scale=float("inf")), dict(out_dtype=2), dict(flags=1 << 9),
-                                 dict(num_splits=-1)])
+                                 dict(num_splits=-1), dict(max_seq_len=2 ** 31 - 70, slot_table_stride=2 ** 31 - 1),
+                                 dict(num_seqs=2000, max_seq_len=2 ** 28, slot_table_stride=2 ** 29, num_heads=64)])
 def test_kv4_plan_refuses(lib, bad):
     assert lib.mla_verify_kv4_plan(ctypes.byref(desc(**bad)), 152, ctypes.byref(m.Plan())) in (-1, -2)
 
