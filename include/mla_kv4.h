@@ -39,8 +39,8 @@ extern "C" {
  * mla_kv4_append -- quantise bf16 latent rows into their slots of a 4-bit pool:
  *   for i < num_rows with slot_map[i] != -1:  pool[slot_map[i]] = row format of rows[i]
  * For each block of 16 latent dims: scale = max|x| / 6 rounded to e4m3 (nearest even, at most
- * 448), code = x / scale rounded to e2m1 (nearest, ties to the even code, at most 6). Both are
- * the roundings of the exact quotients. A block whose scale rounds to 0 (max|x| <= 6 * 2^-10)
+ * 448), code = x / scale rounded to e2m1 (nearest, ties to the even code, at most 6, with x's sign
+ * also where it rounds to 0). Both are the roundings of the exact quotients. A block whose scale rounds to 0 (max|x| <= 6 * 2^-10)
  * has codes 0; magnitudes over 6 * 448 are held as 2688. A block with a NaN or an infinity gets
  * the scale NaN, so all its dims read as NaN. RoPE dims are copied.
  *   pool      device [num_slots][416] bytes, 32-byte aligned (written).

@@ -271,7 +271,7 @@ def kv4_quantise(bits: np.ndarray) -> np.ndarray:
     scale = _nearest_code(np.minimum(top / 6, 448), E4M3)
     s = E4M3[scale][:, :, None]
     y = np.where(fine[:, :, None] & (s > 0), np.where(np.isfinite(x), x, 0) / np.where(s > 0, s, 1), 0)
-    code = _nearest_code(np.minimum(np.abs(y), 6), E2M1) + 8 * (y < 0)
+    code = _nearest_code(np.minimum(np.abs(y), 6), E2M1) + 8 * np.signbit(y)
     code = code.reshape(n, 256, 2).astype(np.uint8)
     out[:, :256] = code[:, :, 0] | (code[:, :, 1] << 4)
     out[:, 256:288] = np.where(fine, scale, 127)

@@ -58,6 +58,20 @@ def odd_rows(n, seed):
     return W.f32_to_bf16_bits(x).reshape(n, 576)
 
 
+@pytest.mark.parametrize("seed", range(3))
+def test_append_writes_exactly_the_defined_bytes(seed):
+    """Every byte of a row, the sign of values that round to zero among them."""
+    import torch
+    import speculative_decode_mla_gb300 as m
+    rng = np.random.default_rng(seed)
+    x = (rng.normal(size=(700, 576)) * np.exp2(rng.integers(-14, 14, size=(700, 1)))).astype(np.float32)
+    x[:, 16:512:16] *= np.float32(2.0 ** 12)                          # the rest of a block far below its largest value
+    bits = np.concatenate([odd_rows(700, 40 + seed).reshape(700, 576), W.f32_to_bf16_bits(x).reshape(700, 576)])
+    pool = torch.zeros(1400, 416, dtype=torch.uint8, device="cuda")
+    m.kv4_append(pool, bf16_dev(bits), torch.arange(1400, dtype=torch.int32, device="cuda"))
+    assert np.array_equal(pool.cpu().numpy(), oracle.kv4_quantise(bits))
+
+
 @pytest.mark.parametrize("n,width", [(1, 576), (2, 584), (15, 1152), (16, 576), (17, 592), (1003, 576)])
 def test_append_then_gather_equals_the_definition(n, width):
     import torch
