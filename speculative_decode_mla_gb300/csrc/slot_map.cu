@@ -5,7 +5,9 @@
 // (num_seqs <= 8192, from L2) instead of waiting for another kernel's sums, then takes its share of
 // the tokens. Nothing that a CTA reads is written by another one: held_out and free_left are separate
 // outputs, the block table is read below have_b and written from there on, the slot table read
-// below h_b and written from there on.
+// below h_b and written from there on. 64 draft trees of 8 nodes with page_size 1 take 4.6 us, 32 prompts of 301 k tokens
+// in pages of 64 take 4.8: launch, then four reads that wait on one another (lengths, the sequence's numbers, block table or
+// free list, slots). With 64-bit divisions it was 5.0 and 5.2.
 #include <atomic>
 
 #include "mla_kv_ops.h"
