@@ -88,8 +88,9 @@ int mla_verify_attn_kv4(const mla_verify_desc *desc, const void *q, const void *
  * The plan is a pure host function of its arguments; the workspace has the layout given there.
  * In the tcgen05 plan chunk_tokens is the least that a pair of CTAs takes at a time: the pairs share
  * the positions of all sequences and row tiles evenly, as the lengths on the device turn out, so a
- * sequence may be cut anywhere, into at most num_splits parts. A total_tokens_hint far above the
- * actual lengths leaves pairs without work; one below them only makes the workspace larger.
+ * sequence may be cut anywhere, into at most num_splits parts. One sequence of at most 128 query
+ * rows is shared evenly whatever its length; otherwise a total_tokens_hint far above the actual
+ * lengths leaves pairs without work, and one below them only makes the workspace larger.
  */
 int mla_verify_kv4_plan(const mla_verify_desc *desc, int32_t num_sms, mla_verify_plan_t *plan);
 int mla_verify_kv4_workspace_size(const mla_verify_desc *desc, size_t *bytes);

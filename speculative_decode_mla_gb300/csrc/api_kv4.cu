@@ -18,6 +18,13 @@ int64_t part_o_bytes(const mla_verify_plan_t& p, int64_t rows) {
   return cdiv((int64_t)p.num_splits * rows * kDLatent * 2, 256) * 256;
 }
 
+// One row tile in all: the pairs may share any length evenly, since it has no more splits than there are pairs, and as
+// many at its greatest length. (A captured call of 128 rows with room for 180 Ki positions
+// takes 18 us at 16 Ki, not 50, and 28 at 64 Ki, not 50.)
+bool shares_any_length(const mla_verify_desc& d, const mla_verify_plan_t& p, int64_t row_tiles) {
+  return p.kernel == 0 && row_tiles == 1 && d.num_splits == 0;
+}
+
 }  // namespace
 }  // namespace mla
 
@@ -50,7 +57,8 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   tiles = tiles < 1 ? 1 : tiles > max_tiles ? max_tiles : tiles;
   if (cdiv(max_tiles, tiles) + 1 > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits - 1);
   p.chunk_tokens = (int32_t)(tiles * tile);
-  if (simt || row_tiles == 1) p.num_splits = (int32_t)cdiv(max_tiles, tiles);
+  if (shares_any_length(*d, p, row_tiles)) p.num_splits = (int32_t)(max_tiles < slots ? max_tiles : slots);
+  else if (simt || row_tiles == 1) p.num_splits = (int32_t)cdiv(max_tiles, tiles);
   else p.num_splits = (int32_t)((max_tiles + tiles - 2) / tiles + 1);  // a row tile may begin inside a share
   if (simt && row_tiles * p.num_splits > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
   const int64_t all = row_tiles * (max_tiles + kKv4SegmentUnits) - kKv4SegmentUnits;
@@ -114,7 +122,7 @@ extern "C" int mla_verify_attn_kv4(const mla_verify_desc* d, const void* q, cons
   a.H = d->num_heads;
   a.stride = d->slot_table_stride;
   a.max_seq_len = d->max_seq_len;
-  a.chunk = p.chunk_tokens;
+  a.chunk = shares_any_length(*d, p, (int64_t)d->num_seqs * p.row_tiles) ? kKv4TileTokens : p.chunk_tokens;
   a.splits = p.num_splits;
   a.row_tiles = p.row_tiles;
   a.rows_per_tile = p.rows_per_tile;

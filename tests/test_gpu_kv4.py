@@ -404,6 +404,31 @@ def test_verify_shares_that_begin_inside_a_sequence(lens, T, H, kw):
     assert_close(call(p, rows, sizes=sizes, **kw), expect(p, bits, sizes=sizes), p.q, bits)
 
 
+@pytest.mark.parametrize("n", [0, 1, 500, 4000, 9600, 9727, 9728, 9729, 20000])
+def test_verify_lengths_far_below_the_limit(n):
+    """One captured call with room for 150,000 positions, replayed for shorter sequences (76 pairs x 128 positions are 9728)."""
+    import torch
+    import speculative_decode_mla_gb300 as m
+    p, rows, bits = problem([20000], 4, 8, 700)
+    room = 150000
+    table = np.zeros((1, room + 4), np.int32)
+    lens = torch.full((1,), room, dtype=torch.int32, device="cuda")
+    dev = (bf16_dev(p.q), to_dev(rows), to_dev(table), lens, to_dev(p.tree_parent))
+    m.verify_kv4(*dev, max_seq_len=room)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = m.verify_kv4(*dev, max_seq_len=room, out_dtype=m.MLA_DTYPE_F32)
+    table[0, :n + 4] = p.slot_table[0, :n + 4]
+    dev[2].copy_(to_dev(table))
+    lens.fill_(n)
+    g.replay()
+    torch.cuda.synchronize()
+    want = oracle.verify(np.array([n], np.int32), table, p.tree_parent, p.q, bits, num_heads=8, scale=W.SOFTMAX_SCALE)
+    got = (out.cpu().numpy().reshape(-1, 512).astype(np.float64), lse.cpu().numpy().reshape(-1).astype(np.float64))
+    assert_close(got, (want[0].reshape(-1, 512), want[1]), p.q, bits, f32=True)
+
+
 @pytest.mark.parametrize("B,T", [(33, 1), (64, 2), (65, 1), (1000, 1), (3000, 2)])
 def test_verify_many_short_sequences(B, T):
     """More sequences than a warp has lanes, most of them one tile: both kernels over the same rows."""
