@@ -8,6 +8,7 @@ namespace {
 
 constexpr int kTcRowsPerTile = 128;  // query rows of a pair of CTAs
 constexpr int kSimtRowsPerTile = 8;  // one warp per row, 8 warps per CTA
+constexpr int kFewRows = 16;         // the rows of one MMA of the kernel for few rows
 constexpr int kMaxSplits = 65535;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -25,6 +26,14 @@ bool shares_any_length(const mla_verify_desc& d, const mla_verify_plan_t& p, int
   return p.kernel == 0 && row_tiles == 1 && d.num_splits == 0;
 }
 
+// The kernel for few rows: at most 16 a sequence, and enough sequences and positions to keep three small CTAs on every SM
+// busy (a lone CTA waits on itself). 16 rows, tcgen05 kernel against this one, us: 4096 sequences of 300 positions 735, 335;
+// 1024 of 300: 208, 122; 256 of 1000: 96, 82; 32 of 8192: 73, 64; 16 of up to 1000: 16.5, 15.0; 4 of 65,536: 71, 61; but 4 of
+// 16,384: 26, 29; 8 of 2000: 15, 18; 1 of 65,536: 27, 37.
+bool takes_few_rows(const mla_verify_desc& d, int64_t rows, int64_t total) {
+  return rows <= kFewRows && !(d.flags & MLA_FLAG_SIMT) && (d.num_seqs >= 16 || (d.num_seqs >= 4 && total >= 131072));
+}
+
 }  // namespace
 }  // namespace mla
 
@@ -37,32 +46,42 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   mla_verify_plan_t p;
   memset(&p, 0, sizeof p);
   const bool simt = (d->flags & MLA_FLAG_SIMT) != 0;
-  p.kernel = simt ? 1 : 0;
-  p.rows_per_tile = simt ? kSimtRowsPerTile : kTcRowsPerTile;
   const int64_t R = (int64_t)d->num_nodes * d->num_heads;
-  p.row_tiles = (int32_t)cdiv(R, p.rows_per_tile);
-  const int64_t tile = simt ? kTileTokens : kKv4TileTokens;
   const int64_t max_n = (int64_t)d->max_seq_len + d->num_nodes;
-  const int64_t max_tiles = cdiv(max_n, tile);
   const int64_t uniform = (int64_t)d->num_seqs * max_n;
   const int64_t total = d->total_tokens_hint > 0 && d->total_tokens_hint < uniform ? d->total_tokens_hint : uniform;
+  const bool few = takes_few_rows(*d, R, total), tc = !simt && !few;
+  p.kernel = simt ? 1 : few ? 2 : 0;
+  p.rows_per_tile = simt ? kSimtRowsPerTile : few ? kFewRows : kTcRowsPerTile;
+  p.row_tiles = (int32_t)cdiv(R, p.rows_per_tile);
+  const int64_t tile = tc ? kKv4TileTokens : kTileTokens;
+  const int64_t max_tiles = cdiv(max_n, tile);
   const int64_t row_tiles = (int64_t)d->num_seqs * p.row_tiles;
   // (the kernels count tiles, and positions of a segment, in 32 bits)
   if (max_n > 0x7fffff00 || (max_tiles + kKv4SegmentUnits) * row_tiles > 0x3fffffff) return MLA_ERR_UNSUPPORTED;
-  // SIMT: units of (sequence, row tile, chunk), small CTAs, several per SM. tcgen05: one cluster per pair of SMs; the
+  // SIMT and few rows: units of (sequence, row tile, chunk), small CTAs, several per SM. tcgen05: one cluster per pair of SMs; the
   // clusters share all tiles equally, at least chunk_tokens / 128 each. That least share only bounds the number of
   // splits that the workspace has room for: the kernel takes the even share of the lengths that it finds.
-  const int64_t slots = simt ? (int64_t)num_sms * 8 : (num_sms / 2 > 0 ? num_sms / 2 : 1);
+  const int64_t slots = simt ? (int64_t)num_sms * 8 : few ? (int64_t)num_sms * 3 : (num_sms / 2 > 0 ? num_sms / 2 : 1);
   int64_t tiles = d->num_splits > 0 ? cdiv(max_tiles, d->num_splits) : cdiv(cdiv(total, tile) * p.row_tiles, slots);
+  if (few && d->num_splits == 0) {
+    // One wave of CTAs (a sequence's last chunk is half empty on average); the merge reads every split, so at most 128 of
+    // them, and four tiles a CTA but for short calls.
+    const int64_t room = slots - d->num_seqs / 2 > 1 ? slots - d->num_seqs / 2 : 1;
+    const int64_t few_tiles = cdiv(max_tiles, 16) < 4 ? cdiv(max_tiles, 16) : 4, few_splits = cdiv(max_tiles, 128);
+    tiles = cdiv(cdiv(total, tile), room);
+    tiles = tiles > few_tiles ? tiles : few_tiles;
+    tiles = tiles > few_splits ? tiles : few_splits;
+  }
   tiles = tiles < 1 ? 1 : tiles > max_tiles ? max_tiles : tiles;
   if (cdiv(max_tiles, tiles) + 1 > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits - 1);
   p.chunk_tokens = (int32_t)(tiles * tile);
   if (shares_any_length(*d, p, row_tiles)) p.num_splits = (int32_t)(max_tiles < slots ? max_tiles : slots);
-  else if (simt || row_tiles == 1) p.num_splits = (int32_t)cdiv(max_tiles, tiles);
+  else if (!tc || row_tiles == 1) p.num_splits = (int32_t)cdiv(max_tiles, tiles);
   else p.num_splits = (int32_t)((max_tiles + tiles - 2) / tiles + 1);  // a row tile may begin inside a share
-  if (simt && row_tiles * p.num_splits > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
+  if (!tc && row_tiles * p.num_splits > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
   const int64_t all = row_tiles * (max_tiles + kKv4SegmentUnits) - kKv4SegmentUnits;
-  p.ctas = (int32_t)(simt ? row_tiles * p.num_splits : 2 * (all < slots ? all : slots));
+  p.ctas = (int32_t)(!tc ? row_tiles * p.num_splits : 2 * (all < slots ? all : slots));
   const int64_t rows = (int64_t)d->num_seqs * R;
   p.workspace_bytes = part_o_bytes(p, rows) + cdiv((int64_t)p.num_splits * rows * 4, 256) * 256;
   *plan = p;
@@ -132,7 +151,10 @@ extern "C" int mla_verify_attn_kv4(const mla_verify_desc* d, const void* q, cons
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
-  if ((p.kernel == 1 ? launch_verify_kv4_simt(a, s) : launch_verify_kv4_tc(a, p.ctas, s)) != cudaSuccess) return MLA_ERR_CUDA;
+  if ((p.kernel == 1   ? launch_verify_kv4_simt(a, s)
+       : p.kernel == 2 ? launch_verify_kv4_rows(a, s)
+                       : launch_verify_kv4_tc(a, p.ctas, s)) != cudaSuccess)
+    return MLA_ERR_CUDA;
   if (launch_combine(p.num_splits, a.rows, kDLatent, a.part_o, MLA_DTYPE_F16, a.part_lse, out, lse, d->out_dtype,
                      /*dependent=*/true, s) != cudaSuccess)
     return MLA_ERR_CUDA;

@@ -47,6 +47,7 @@ struct VerifyArgs {
 cudaError_t launch_verify_simt(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_verify_tc(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_verify_kv4_simt(const VerifyArgs& a, cudaStream_t stream);  // kv: the 4-bit pool
+cudaError_t launch_verify_kv4_rows(const VerifyArgs& a, cudaStream_t stream);  // at most 16 rows a sequence
 cudaError_t launch_verify_kv4_tc(const VerifyArgs& a, int32_t ctas, cudaStream_t stream);  // chunk: a cluster's least share
 // part_dtype: MLA_DTYPE_F32 or MLA_DTYPE_F16. With `dependent`, the launch may start while the
 // preceding kernel on the stream finishes (programmatic dependent launch); the kernel waits

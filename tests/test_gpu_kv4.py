@@ -390,11 +390,11 @@ MANY = [int(x) for x in np.random.default_rng(5).integers(0, 900, size=100)]
 
 
 @pytest.mark.parametrize("lens,T,H,kw", [
-    (MANY, 2, 3, {}), (MANY, 2, 3, dict(num_splits=1)), (MANY, 2, 3, dict(num_splits=3, total_tokens_hint=1)),
+    (MANY, 2, 9, {}), (MANY, 2, 9, dict(num_splits=1)), (MANY, 2, 9, dict(num_splits=3, total_tokens_hint=1)),
     ([900, 0, 3000, 1500], 16, 20, {}), ([900, 0, 3000, 1500], 16, 20, dict(num_splits=1)),
     ([900, 0, 3000, 1500], 16, 20, dict(num_splits=2)), ([900, 0, 3000, 1500], 16, 20, dict(total_tokens_hint=10 ** 9)),
-    ([5] * 33 + [6000], 5, 29, {}), ([5] * 33 + [6000], 5, 29, dict(num_splits=1)), ([0] * 70, 1, 1, {}),
-    ([200, 1] * 80, 1, 2, dict(total_tokens_hint=300)),
+    ([5] * 33 + [6000], 5, 29, {}), ([5] * 33 + [6000], 5, 29, dict(num_splits=1)), ([0] * 70, 1, 17, {}),
+    ([200, 1] * 80, 1, 20, dict(total_tokens_hint=300)),
 ], ids=lambda x: str(len(x)) if isinstance(x, list) else None)
 def test_verify_shares_that_begin_inside_a_sequence(lens, T, H, kw):
     """A pair of CTAs takes a run of tiles that may hold several sequences and row tiles, whole or in part."""
@@ -429,24 +429,90 @@ def test_verify_lengths_far_below_the_limit(n):
     assert_close(got, (want[0].reshape(-1, 512), want[1]), p.q, bits, f32=True)
 
 
-@pytest.mark.parametrize("B,T", [(33, 1), (64, 2), (65, 1), (1000, 1), (3000, 2)])
-def test_verify_many_short_sequences(B, T):
+@pytest.mark.parametrize("B,T,H", [(33, 1, 3), (33, 1, 17), (64, 2, 9), (65, 1, 17), (65, 1, 3), (1000, 1, 17), (3000, 2, 9), (3000, 2, 3)])
+def test_verify_many_short_sequences(B, T, H):
     """More sequences than a warp has lanes, most of them one tile: both kernels over the same rows."""
     import speculative_decode_mla_gb300 as m
     rng = np.random.default_rng(B)
     lens = [int(x) for x in np.where(rng.random(B) < 0.8, rng.integers(0, 100, B), rng.integers(100, 700, B))]
-    p, rows, bits = problem(lens, T, 3, 600 + B)
+    p, rows, bits = problem(lens, T, H, 600 + B)
     got, ref = call(p, rows, out_dtype=m.MLA_DTYPE_F32), call(p, rows, out_dtype=m.MLA_DTYPE_F32, flags=m.MLA_FLAG_SIMT)
     assert_close(got, ref, p.q, bits, f32=True)
     if B <= 65:
         assert_close(got, expect(p, bits), p.q, bits, f32=True)
 
 
+FEW = [0, 1, 31, 32, 33, 63, 64, 65, 100, 300, 1000, 127, 128, 129, 5, 2500, 17, 700]
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 16), (16, 1), (2, 8), (3, 5), (5, 3)])
+@pytest.mark.parametrize("kw", [{}, dict(num_splits=1), dict(num_splits=9), dict(total_tokens_hint=1)], ids=["plan", "one", "nine", "hint"])
+def test_verify_few_rows(T, H, kw):
+    """At most 16 rows a sequence and many sequences: the kernel for few rows."""
+    import speculative_decode_mla_gb300 as m
+    p, rows, bits = problem(FEW, T, H, 800 + T)
+    d = m.make_desc(p.B, T, H, p.num_slots, p.slot_table.shape[1], p.max_seq_len)
+    assert m.kv4_plan(d, 152).kernel == 2
+    assert_close(call(p, rows, out_dtype=m.MLA_DTYPE_F32, **kw), expect(p, bits), p.q, bits, f32=True)
+    sizes = 1 + np.arange(p.B) % T
+    got, want = call(p, rows, sizes=sizes, **kw), expect(p, bits, sizes=sizes)
+    assert_close(got, want, p.q, bits)
+    assert (got[0][np.isneginf(want[1])] == 0).all()
+
+
+def test_verify_few_rows_of_any_size_with_nan_and_infinities():
+    p, rows, bits = problem(FEW, 4, 4, 810)
+    x = W.bf16_bits_to_f32(p.q).copy()
+    x[0::4] *= np.float32(2.0 ** -100)
+    x[1::4] *= np.float32(8)
+    x[2::4, :, :512] *= np.float32(2.0 ** -25)
+    x[3::4] = 0
+    q = W.f32_to_bf16_bits(x).reshape(p.q.shape)
+    want = expect(p, bits, q=q)
+    assert_close(call(p, rows, q=q), want, q, bits)
+    bad = rows.copy()
+    parents = np.tile(np.array([-1, 0, 0, 2], np.int32), (p.B, 1))
+    want = expect(p, bits, parents=parents)
+    clean = np.ones(p.rows, bool)
+    for b in (3, 10):
+        bad[p.slot_table[b, p.seq_lens[b] + 1], 256 + 7] = 0x7F       # node 1: NaN in a block; only node 1 sees it
+        bad[p.slot_table[b, p.seq_lens[b] + 2], 288:].view(np.uint16)[:] = 0x7F80   # node 2: infinite RoPE dims (2 and 3)
+        clean[(b * 4 + 1) * 4:(b * 4 + 4) * 4] = False
+    bad[p.slot_table[15, 700], 256] = 0xFF                            # a prefix position of one sequence
+    clean[15 * 16:16 * 16] = False
+    o, l = call(p, bad, parents=parents)
+    assert_close((o[clean], l[clean]), (want[0][clean], want[1][clean]), p.q, bits)
+    s, sl = call(p, bad, parents=parents, flags=2)
+    assert np.isnan(l[~clean]).all() and np.array_equal(np.isnan(s), np.isnan(o))
+
+
+def test_verify_few_rows_checks_slots_and_repeatability():
+    import torch
+    import speculative_decode_mla_gb300 as m
+    p, rows, bits = problem(FEW, 2, 8, 820)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(flags=m.MLA_FLAG_DEBUG_CHECKS, dev_status=st)
+    a = call(p, rows, **kw)
+    perm = np.random.default_rng(1).permutation(p.num_slots)
+    moved = np.empty_like(rows)
+    moved[perm] = rows
+    b = call(p, moved, table=perm[p.slot_table].astype(np.int32))
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    table, parents = p.slot_table.copy(), p.tree_parent.copy()
+    table[15, 2400] = -7
+    parents[17, 1] = 1
+    for bad, flag in ((dict(table=table), m.CHECK_BAD_SLOT), (dict(parents=parents), m.CHECK_BAD_PARENT),
+                      (dict(max_seq_len=2499), m.CHECK_BAD_LENGTH), (dict(sizes=[3] * p.B), m.CHECK_BAD_LENGTH)):
+        with pytest.raises(m.MLAError):
+            call(p, rows, **kw, **bad)
+        assert st.item() == flag
+
+
 def test_debug_checks_of_the_last_sequences():
     """Bad slots and parents that only a cluster's later sequences hold are reported too."""
     import torch
     import speculative_decode_mla_gb300 as m
-    p, rows, bits = problem(MANY, 2, 3, 51)
+    p, rows, bits = problem(MANY, 2, 9, 51)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     kw = dict(flags=m.MLA_FLAG_DEBUG_CHECKS, dev_status=st, num_splits=1)
     assert_close(call(p, rows, **kw), expect(p, bits), p.q, bits)

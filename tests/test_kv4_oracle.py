@@ -170,7 +170,7 @@ def test_kv4_plan_covers_every_position(lib, kw):
     n = d.max_seq_len + d.num_nodes
     # a row tile's positions may begin inside a share of chunk_tokens; a single one is shared by all 76 pairs of SMs
     cover = -(-n // p.chunk_tokens)
-    most = cover if p.kernel == 1 else max(cover + 2, min(-(-n // 128), 76))
+    most = cover if p.kernel else max(cover + 2, min(-(-n // 128), 76))
     assert p.chunk_tokens % 64 == 0 and cover <= p.num_splits <= most
     assert p.row_tiles * p.rows_per_tile >= d.num_nodes * d.num_heads
     rows = d.num_seqs * d.num_nodes * d.num_heads
