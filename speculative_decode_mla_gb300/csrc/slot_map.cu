@@ -218,18 +218,18 @@ extern "C" int mla_slot_map_build(const int32_t* seq_lens, const int32_t* new_le
     return MLA_ERR_INVALID_ARGUMENT;
   if (debug && !dev_status) return MLA_ERR_INVALID_ARGUMENT;
 
-  const size_t smem = ((size_t)2 * num_seqs + 1) * sizeof(int32_t);
-  if (smem > 48 * 1024) {  // the opt-in is set once per device (setting it twice is harmless)
-    static std::atomic<bool> configured[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_NO_DEVICE;
-    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-      if (cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (2 * kMapMaxSeqs + 1) * (int)sizeof(int32_t)) != cudaSuccess)
-        return MLA_ERR_CUDA;
-      if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
-    }
+  // The opt-in to more than the default limit (48 KB of dynamic and static bytes together, from 6112 sequences on), set
+  // once per device whatever this call needs (setting it twice is harmless).
+  static std::atomic<bool> configured[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MLA_ERR_NO_DEVICE;
+  if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (2 * kMapMaxSeqs + 1) * (int)sizeof(int32_t)) != cudaSuccess)
+      return MLA_ERR_CUDA;
+    if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
   }
+  const size_t smem = ((size_t)2 * num_seqs + 1) * sizeof(int32_t);
   const int64_t per_cta = (int64_t)kMapThreads * kMapTokens;
   const int64_t want = (map_capacity + per_cta - 1) / per_cta;
   const unsigned ctas = (unsigned)(want < 1 ? 1 : want > 608 ? 608 : want);
