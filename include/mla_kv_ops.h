@@ -123,8 +123,10 @@ int mla_kv_compact(const void *src_pool, int64_t src_slots, void *dst_pool, int6
  *   slot_table          device int32 [num_seqs][slot_stride].
  *   slot_map            device int32 [map_capacity].
  *   cu_new              device int32 [num_seqs + 1].
- *   held_out, free_left device int32 [num_seqs] and [1]; they must not be held_lens (or seq_lens)
- *                       and free_count themselves: inputs are not written.
+ *   held_out, free_left device int32 [num_seqs] and [1].
+ * Inputs are not written, and no array that is written (the tables, the outputs, dev_status under debug) may
+ * overlap another array of the call: MLA_ERR_INVALID_ARGUMENT. Inputs may be the same array as one another, and with
+ * page_size 1 block_table may be slot_table itself (they hold the same numbers then).
  * page_size >= 1 and num_pages * page_size <= 2^31 - 1; map_capacity <= 2^31 - 1.
  */
 int mla_slot_map_build(const int32_t *seq_lens, const int32_t *new_lens, const int32_t *held_lens, int32_t num_seqs,

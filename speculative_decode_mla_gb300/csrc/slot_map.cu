@@ -4,8 +4,8 @@
 // what counts is the latency of one kernel: every CTA sums the lengths of all sequences for itself
 // (num_seqs <= 8192, from L2) instead of waiting for another kernel's sums, then takes its share of
 // the tokens. Nothing that a CTA reads is written by another one: held_out and free_left are separate
-// outputs, the block table is read below have_b and written from there on, the slot table read
-// below h_b and written from there on. 64 draft trees of 8 nodes with page_size 1 take 4.6 us, 32 prompts of 301 k tokens
+// outputs (overlapping arrays are refused), the block table is read below have_b and written from there on, the slot
+// table read below h_b and written from there on. 64 draft trees of 8 nodes with page_size 1 take 4.6 us, 32 prompts of 301 k tokens
 // in pages of 64 take 4.8: launch, then four reads that wait on one another (lengths, the sequence's numbers, block table or
 // free list, slots). With 64-bit divisions it was 5.0 and 5.2.
 #include <atomic>
@@ -22,6 +22,15 @@ constexpr int kMapMaxSeqs = 8192;
 constexpr int kMapTokens = 4;  // consecutive tokens a thread takes at a time (one 16-byte store to the map)
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Span {  // an array of int32
+  const int32_t* p;
+  int64_t n;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.n > 0 && b.n > 0 && x < y + 4 * (uintptr_t)b.n && y < x + 4 * (uintptr_t)a.n;
+}
 
 struct MapArgs {
   const int32_t *seq_lens, *new_lens, *held_lens, *free_pages, *free_count;
@@ -214,9 +223,20 @@ extern "C" int mla_slot_map_build(const int32_t* seq_lens, const int32_t* new_le
                         slot_map, cu_new,   held_out,  free_left,  dev_status};
   for (const void* p : ptrs)
     if (!aligned(p, 4)) return MLA_ERR_INVALID_ARGUMENT;
-  if (held_out == held_lens || held_out == seq_lens || held_out == new_lens || free_left == free_count)
-    return MLA_ERR_INVALID_ARGUMENT;
   if (debug && !dev_status) return MLA_ERR_INVALID_ARGUMENT;
+  // What is written (the tables too) lies over nothing else: CTAs read the inputs, and the tables' old parts, at any time.
+  // (With pages of one slot both tables hold the same numbers, and one array may serve as both: a thread writes its
+  // place twice, the slot last.)
+  const int64_t B = num_seqs;
+  const bool one_table = page_size == 1 && block_table == slot_table && block_stride == slot_stride;
+  const Span spans[] = {{block_table, block_table && !one_table ? B * block_stride : 0}, {slot_table, B * slot_stride},
+                        {slot_map, map_capacity}, {cu_new, B + 1}, {held_out, B}, {free_left, 1},
+                        {dev_status, debug ? 1 : 0},  // the first seven are written
+                        {seq_lens, B}, {new_lens, B}, {held_lens, held_lens ? B : 0}, {free_pages, free_capacity},
+                        {free_count, 1}};
+  for (int i = 0; i < 7; ++i)
+    for (const Span& other : spans)
+      if (&other != &spans[i] && overlap(spans[i], other)) return MLA_ERR_INVALID_ARGUMENT;
 
   // The opt-in to more than the default limit (48 KB of dynamic and static bytes together, from 6112 sequences on), set
   // once per device whatever this call needs (setting it twice is harmless).
