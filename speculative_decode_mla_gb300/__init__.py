@@ -470,8 +470,9 @@ def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, 
         _check_tensor("dev_status", dev_status, i32, (1,), dev)
     raw, here = _on(dev, stream)
     with here:
-        desc, need = _kv4_desc(dev, B, T, H, slots, stride, max_seq_len, softmax_scale,
-                               out_dtype, DEFAULT_FLAGS if flags is None else flags, num_splits, total_tokens_hint)
+        # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
+        desc, need = _kv4_desc(dev, B, T, H, slots, stride, int(max_seq_len), float(softmax_scale), int(out_dtype),
+                               int(DEFAULT_FLAGS if flags is None else flags), int(num_splits), int(total_tokens_hint))
         if out is None:
             out = torch.empty((B * T, H, D_LATENT), device=q.device, dtype=out_type)
         else:
