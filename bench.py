@@ -131,9 +131,9 @@ class ClockSampler:
         return {"sm_mhz": statistics.median(sm), "sm_max_mhz": mx, "reasons": sorted(reasons), "samples": len(sm)}
 
 
-# the files the tcgen05 attention kernel is built from (with the headers): the ncu traffic
-# record below is only used while they are unchanged
-TC_SOURCES = ["verify_tc.cu", "tc.cuh", "common.cuh"]
+# the files the tcgen05 attention kernel is built from: the ncu traffic record below is only
+# used while they are unchanged
+TC_SOURCES = ["verify_tc.cu", "tc.cuh", "common.cuh", "mla_verify.h"]
 
 
 def traffic_record(fingerprint):

@@ -28,15 +28,14 @@ def _sources():
 
 
 def source_fingerprint(names=None) -> str:
-    """Hash of the compile flags and of the named csrc files (all sources when None) plus every
-    header, by file name and contents, so it is the same wherever the tree is checked out."""
+    """Hash of the compile flags and of the named files of csrc and include (all sources and headers when None), by file
+    name and contents, so it is the same wherever the tree is checked out."""
     h = hashlib.sha256()
     h.update(" ".join(f for f in FLAGS if not os.path.isabs(f)).encode())
     if names is None:
-        files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
+        files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     else:
-        files = [os.path.join(CSRC, n) for n in names]
-    files += sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+        files = [next(p for p in (os.path.join(CSRC, n), os.path.join(INCLUDE, n)) if os.path.exists(p)) for n in names]
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
