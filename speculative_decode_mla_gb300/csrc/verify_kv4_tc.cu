@@ -895,22 +895,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         xch[(gt & 1) * 128 + l128] = mt;
         row_pair_sync(q4);
         if (!ok) continue;
-        mt = fmaxf(mt, xch[(gt & 1) * 128 + (l128 ^ 64)]) * unscale;
+        // The running maximum is kept as the scores come, before their scale, and taken away before the product: the key that
+        // set it weighs 2^kPBias to the bit however large the scores are. (One fma, the exact product less the rounded
+        // product of the maximum, is off by half an ulp of it: from 2^27 on that put weights anywhere from 0 to infinity.)
+        mt = fmaxf(mt, xch[(gt & 1) * 128 + (l128 ^ 64)]);
         bool rescale = false;
         float alpha = 1.f;
-        if (mt > m_run + 8.f || m_run == -INFINITY) {
-          alpha = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
+        if ((mt - m_run) * unscale > 8.f || m_run == -INFINITY) {
+          alpha = m_run == -INFINITY ? 0.f : ex2((m_run - mt) * unscale);
           rescale = t > 0 && m_run != mt;
           l_run *= alpha;
           m_run = mt;
         }
-        const float neg_m = m_run == -INFINITY ? 0.f : kPBias - m_run;
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
         uint32_t pk[32];
         float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < 64; k += 4) {
-          const float2 x0 = fma2(make_float2(sc[k], sc[k + 1]), make_float2(unscale, unscale), make_float2(neg_m, neg_m));
-          const float2 x1 = fma2(make_float2(sc[k + 2], sc[k + 3]), make_float2(unscale, unscale), make_float2(neg_m, neg_m));
+          const float2 d0 = add2(make_float2(sc[k], sc[k + 1]), make_float2(neg_m, neg_m));
+          const float2 d1 = add2(make_float2(sc[k + 2], sc[k + 3]), make_float2(neg_m, neg_m));
+          const float2 x0 = fma2(d0, make_float2(unscale, unscale), make_float2(kPBias, kPBias));
+          const float2 x1 = fma2(d1, make_float2(unscale, unscale), make_float2(kPBias, kPBias));
           const float2 e0 = make_float2(ex2(x0.x), ex2(x0.y)), e1 = make_float2(ex2(x1.x), ex2(x1.y));
           const __half2 h0 = __floats2half2_rn(e0.x, e0.y), h1 = __floats2half2_rn(e1.x, e1.y);
           pk[k / 2] = *reinterpret_cast<const uint32_t*>(&h0);
@@ -958,7 +963,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
         const int row = s[1] * kRows + (int)rank * kCtaRows + r;
         if (ok && row < R)
           a.part_lse[(int64_t)s[2] * a.rows + (int64_t)s[0] * R + row] =
-              row >= s[7] * a.H || l == 0.f ? -INFINITY : (m_run + (log2f(l) - kPBias)) * 0.6931471805599453f;
+              row >= s[7] * a.H || l == 0.f ? -INFINITY : (m_run * unscale + (log2f(l) - kPBias)) * 0.6931471805599453f;
       }
       __syncwarp();
       asm volatile("bar.arrive 3, %0;" ::"n"(32 * (kGatherWarps + 4)) : "memory");
