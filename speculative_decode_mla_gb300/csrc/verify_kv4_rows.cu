@@ -15,7 +15,7 @@
 // with three on an SM) and the issue slots (44% of them in use); tensor pipe 29%, DRAM 19%. MMAs of one key after another
 // instead of interleaved took 5 to 8% longer, two CTAs on an SM without spills 25% (here: 8 bytes spilled).
 //   16 rows: 32 sequences of 8192 positions 64 us, 1024 of 300 122 us, 4096 of 300 335 us (8 rows), merge included
-// Rounding as in verify_kv4_tc.cu: Q's rows scaled by a power of two, P = 2^(s - m + 7) in fp16, l from unrounded weights.
+// Rounding as in verify_kv4_tc.cu: Q's rows and the keys scaled by powers of two (kv4.cuh), P = 2^(s - m + 7) in fp16, l from unrounded weights.
 #include <atomic>
 
 #include "kv4.cuh"
@@ -147,14 +147,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3) verify_kv4_rows_kernel(const V
       uint32_t x = 0u;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) x = max(x, s_top[w][row]);
-      const int e = (int)(x >> 7), k2 = min(110, (e == 0 || e == 255) ? 0 : 141 - e);  // as in verify_kv4_tc.cu
-      const float up = __int_as_float((127 + k2) << 23);
-      unscale[h] = __int_as_float((127 - k2) << 23) * a.scale_log2;
+      const int k2 = query_shift(x);
+      const float up = exp2i(k2);
+      unscale[h] = score_scale(k2, a.scale_log2);
 #pragma unroll
       for (int k = 0; k < 9; ++k)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float lo = __uint_as_float(q[k][h + i] << 16) * up, hi = __uint_as_float(q[k][h + i] & 0xffff0000u) * up;
+          const float f = k < 8 ? up : up * exp2i(-kKeyShift);
+          const float lo = __uint_as_float(q[k][h + i] << 16) * f, hi = __uint_as_float(q[k][h + i] & 0xffff0000u) * f;
           if (k < 8) {
             q[k][h + i] = pack_half2(lo, hi);
           } else {
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) verify_kv4_rows_kernel(const V
     for (int j = 0; j < kKeys / 8; ++j) {
       const int key = 8 * j + g;
       w[j] = *reinterpret_cast<const uint4*>(st + (key >> 1) * 128 + ((((key & 1) * 4 + t) ^ (((key >> 1) & 3) << 1)) << 4));
-      sc[j] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kCodes + key * 8 + 2 * t));
+      sc[j] = key_scales(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(st + kCodes + key * 8 + 2 * t)));
       const uint2 r = *reinterpret_cast<const uint2*>(st + kCodes + kScales + key * 32 + 8 * t);
 #pragma unroll
       for (int k = 0; k < 4; ++k) c[j][k] = 0.f;

@@ -16,8 +16,7 @@
 // so CTA r dequantises its own 64 rows whole and of the partner's 64 rows the 256 value dims
 // that it supplies. Codes x scales are exact in fp16, so K, V and Q are fp16 operands; the RoPE dims
 // stay bf16 (kind::f16 takes either, and both accumulate into the same fp32 scores). A query row is
-// scaled by a power of two so that its largest magnitude lies in [2^14, 2^15): its bf16 values are then exact
-// in fp16 down to 2^-29 of the largest, and the scale is taken out of the scores.
+// scaled by a power of two, the keys by another (kv4.cuh), and both are taken out of the scores.
 //
 //   warps 0-15   gather and dequantise: eight threads a key. Codes go from global memory through registers
 //                (loads of a tile are out before the one before it is used), cvt e2m1x2 -> f16x2, times the block's
@@ -492,18 +491,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         load_own(row_of(own), true);
-        // top is in [2^(e - 127), 2^(e - 126)): k2 = 14 - (e - 127); rows of zeros, infinities or NaN stay as they are
-        const int e = (int)(top >> 7);
-        const int k2 = min(110, (e == 0 || e == 255) ? 0 : 141 - e);  // (2^-k2 stays a normal fp32 number)
-        const float up = __int_as_float((127 + k2) << 23);
-        if (pc == 0) s_scale[key] = __int_as_float((127 - k2) << 23) * a.scale_log2;
+        const int k2 = query_shift(top);
+        const float up = exp2i(k2);
+        if (pc == 0) s_scale[key] = score_scale(k2, a.scale_log2);
         const uint32_t jj = (uint32_t)pc & 3u;
 #pragma unroll
         for (int m = 0; m < 9; ++m) {
           uint32_t x[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float lo = __uint_as_float(qv[m][k] << 16) * up, hi = __uint_as_float(qv[m][k] & 0xffff0000u) * up;
+            const float f = m < 8 ? up : up * exp2i(-kKeyShift);
+            const float lo = __uint_as_float(qv[m][k] << 16) * f, hi = __uint_as_float(qv[m][k] & 0xffff0000u) * f;
             if (m < 8) {
               const __half2 h = __floats2half2_rn(lo, hi);
               x[k] = *reinterpret_cast<const uint32_t*>(&h);
@@ -540,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
           for (int i = 0; i < 2; ++i) {
             ok = ok && wait_warp(bar(kBarKEmpty + k_slot), k_par ^ 1u, abort_flag);
             if (!ok) break;
-            dequant_piece(kc.c + 4 * i, e4m3x2_to_f16x2(i ? kc.s >> 16 : kc.s), false, k_at + k_slot * kKSlotBytes);
+            dequant_piece(kc.c + 4 * i, key_scales(e4m3x2_to_f16x2(i ? kc.s >> 16 : kc.s)), false, k_at + k_slot * kKSlotBytes);
             if (i == 1) {
               // (the slot of the S before's second half is two back, or one on)
               ok = wait_warp(bar(kBarKEmpty + (k_slot == 2 ? 0 : k_slot + 1)), k_slot == 2 ? k_par : k_par ^ 1u, abort_flag);

@@ -66,3 +66,38 @@ def check(kernel, q_size, k_size, scale=W.SOFTMAX_SCALE):
 @pytest.mark.parametrize("power", [16, 24, 27, 28, 29, 33, 48, 80, 100])
 def test_scores_far_beyond_the_weights_range(kernel, power):
     check(kernel, 1.0, 2.0 ** power)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("q_size,k_size", [(1.0, 2.0 ** 113), (1.0, 2.0 ** 125), (2.0 ** -20, 2.0 ** 127), (2.0 ** -100, 2.0 ** 127),
+                                           (2.0 ** 60, 2.0 ** 64), (2.0 ** 126, 1.0)])
+def test_keys_and_queries_up_to_the_types_largest(kernel, q_size, k_size):
+    check(kernel, q_size, k_size)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("power", [-131, -127, -121, -100])
+def test_the_smallest_queries_with_the_largest_keys(kernel, power):
+    """Query rows from bf16's subnormals on against RoPE keys near its largest, so that the scores are ordinary. A weight and a part's
+    output are rounded to fp16 (2^-11 each), the rest is fp32: a score is off by at most 576 * 2^-24 of the sum of its products'
+    magnitudes (64 of at most 4 * 4 * 16 times the scale of 0.072: below 64 * 2^5), which moves the lse and, with the norm, weights
+    by twice as much."""
+    import torch
+    import speculative_decode_mla_gb300 as m
+    lens, T, H, number, splits = KERNELS[kernel]
+    p = W.custom_problem(lens, T, H, seed=97, pool_slack=5)
+    x = W.bf16_bits_to_f32(W.normal_bf16(98, p.num_slots * 576)).reshape(p.num_slots, 576).copy()
+    k_size, q_size = (2.0 ** 124, 2.0 ** power) if power < -118 else (2.0 ** (4 - power), 2.0 ** power)
+    x[:, 512:] = np.clip(x[:, 512:], -4, 4) * np.float32(k_size)
+    q = W.bf16_bits_to_f32(p.q).copy()
+    q = W.f32_to_bf16_bits(np.clip(q, -4, 4) * np.float32(q_size)).reshape(p.q.shape)
+    rows = oracle.kv4_quantise(W.f32_to_bf16_bits(x))
+    o, l = oracle.verify(p.seq_lens, p.slot_table, p.tree_parent, q, oracle.kv4_bf16(rows), num_heads=H, scale=W.SOFTMAX_SCALE)
+    out, lse = m.verify_kv4(bf16_dev(q), to_dev(rows), to_dev(p.slot_table), to_dev(p.seq_lens), to_dev(p.tree_parent),
+                            max_seq_len=p.max_seq_len, out_dtype=m.MLA_DTYPE_F32, num_splits=splits,
+                            flags=m.MLA_FLAG_SIMT if number == 1 else None)
+    torch.cuda.synchronize()
+    d_score = 576 * 2.0 ** -24 * 64 * 2.0 ** 5
+    top = np.abs(oracle.kv4_values(rows)[:, :512]).max()
+    assert np.abs(lse.cpu().numpy().reshape(-1) - l.reshape(-1)).max() <= d_score
+    assert np.abs(out.cpu().numpy().reshape(-1, 512) - o.reshape(-1, 512)).max() <= (2 * 2.0 ** -11 + 2 * d_score) * top
