@@ -86,8 +86,9 @@ int mla_verify_attn_kv4(const mla_verify_desc *desc, const void *q, const void *
  * mla_verify_kv4_plan, mla_verify_kv4_workspace_size -- the launch plan and the workspace bytes of
  * mla_verify_attn_kv4 (mla_verify_plan and mla_verify_workspace_size describe the bf16 kernels).
  * The plan is a pure host function of its arguments; the workspace has the layout given there.
- * plan->kernel is 2 for the kernel that calls with few query rows a sequence and many sequences take; its
- * chunks are fixed, as in the SIMT plan. In the tcgen05 plan (0) chunk_tokens is the least that a pair of CTAs takes at a time: the pairs share
+ * plan->kernel is 2 for the kernel that calls with at most 16 query rows a sequence and many sequences of
+ * fairly even lengths (max_seq_len against total_tokens_hint) take; its chunks are fixed, as in the SIMT plan.
+ * In the tcgen05 plan (0) chunk_tokens is the least that a pair of CTAs takes at a time: the pairs share
  * the positions of all sequences and row tiles evenly, as the lengths on the device turn out, so a
  * sequence may be cut anywhere, into at most num_splits parts. One sequence of at most 128 query
  * rows is shared evenly whatever its length; otherwise a total_tokens_hint far above the actual

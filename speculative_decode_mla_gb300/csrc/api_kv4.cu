@@ -27,11 +27,32 @@ bool shares_any_length(const mla_verify_desc& d, const mla_verify_plan_t& p, int
 }
 
 // The kernel for few rows: at most 16 a sequence, and enough sequences and positions to keep three small CTAs on every SM
-// busy (a lone CTA waits on itself). 16 rows, tcgen05 kernel against this one, us: 4096 sequences of 300 positions 735, 335;
-// 1024 of 300: 208, 122; 256 of 1000: 96, 82; 32 of 8192: 73, 64; 16 of up to 1000: 16.5, 15.0; 4 of 65,536: 71, 61; but 4 of
-// 16,384: 26, 29; 8 of 2000: 15, 18; 1 of 65,536: 27, 37.
-bool takes_few_rows(const mla_verify_desc& d, int64_t rows, int64_t total) {
-  return rows <= kFewRows && !(d.flags & MLA_FLAG_SIMT) && (d.num_seqs >= 16 || (d.num_seqs >= 4 && total >= 131072));
+// busy (a lone CTA waits on itself). 16 rows, equal lengths, tcgen05 kernel against this one, us: 4096 sequences of 300 positions
+// 827, 433; 1024 of 300: 210, 123; 256 of 1000: 97, 83; 32 of 8192: 75, 65; 16 of up to 1000: 16.5, 15.0; 4 of 65,536: 70, 61;
+// but 4 of 16,384: 26, 29; 8 of 2000: 15, 18; 1 of 65,536: 27, 37.
+// Its chunks are fixed and walked by one CTA each, on a grid that has room for every sequence at the greatest length, where the
+// tcgen05 kernel's pairs share all positions. So the lengths have to be even, as far as the hint tells: the longest at most 2.25
+// times the mean, or chunks of at most 1.5 times an even share of all positions and at most four CTAs for every place on the SMs.
+// One of 131,072 among 1000 of 300: 238, 5461 us; one of 16,384: 209, 764; one of 32,000 among 64 of 1000: 43, 96 (chunks of 1.2 times
+// the share, 18 CTAs a place); 512 between 300 and 9600: 380, 482 (2.3 times the share); 4 between 16,384 and 65,536: 45, 55 (1.8). On the
+// other side 128 between 300 and 9600: 103, 89; 16 of 65,536 with room for 184,320: 249, 190; 1024 of up to 8000: 1041, 954.
+bool takes_few_rows(const mla_verify_desc& d, int64_t total, int64_t uniform, int64_t max_tiles, int64_t tiles, int64_t slots) {
+  if ((int64_t)d.num_nodes * d.num_heads > kFewRows || (d.flags & MLA_FLAG_SIMT)) return false;
+  if (d.num_seqs < 4 || (d.num_seqs < 16 && total < 131072)) return false;
+  if (d.num_seqs >= 8 && 4 * uniform <= 9 * total) return true;
+  return 2 * tiles * slots <= 3 * cdiv(total, kTileTokens) && d.num_seqs * cdiv(max_tiles, tiles) <= 4 * slots;
+}
+
+// Tiles of 64 positions to a chunk of the kernel for few rows: one wave of CTAs (a sequence's last chunk is half empty on average);
+// the merge reads every split, so at most 128 of them, and four tiles a CTA but for short calls.
+int64_t few_rows_tiles(const mla_verify_desc& d, int64_t total, int64_t max_tiles, int64_t slots) {
+  if (d.num_splits > 0) return cdiv(max_tiles, d.num_splits);
+  const int64_t room = slots - d.num_seqs / 2 > 1 ? slots - d.num_seqs / 2 : 1;
+  const int64_t few_tiles = cdiv(max_tiles, 16) < 4 ? cdiv(max_tiles, 16) : 4, few_splits = cdiv(max_tiles, 128);
+  int64_t tiles = cdiv(cdiv(total, kTileTokens), room);
+  tiles = tiles > few_tiles ? tiles : few_tiles;
+  tiles = tiles > few_splits ? tiles : few_splits;
+  return tiles > max_tiles ? max_tiles : tiles;
 }
 
 }  // namespace
@@ -50,7 +71,9 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   const int64_t max_n = (int64_t)d->max_seq_len + d->num_nodes;
   const int64_t uniform = (int64_t)d->num_seqs * max_n;
   const int64_t total = d->total_tokens_hint > 0 && d->total_tokens_hint < uniform ? d->total_tokens_hint : uniform;
-  const bool few = takes_few_rows(*d, R, total), tc = !simt && !few;
+  const int64_t few_slots = (int64_t)num_sms * 3, few_max = cdiv(max_n, kTileTokens);
+  const int64_t few_tiles = few_rows_tiles(*d, total, few_max, few_slots);
+  const bool few = takes_few_rows(*d, total, uniform, few_max, few_tiles, few_slots), tc = !simt && !few;
   p.kernel = simt ? 1 : few ? 2 : 0;
   p.rows_per_tile = simt ? kSimtRowsPerTile : few ? kFewRows : kTcRowsPerTile;
   p.row_tiles = (int32_t)cdiv(R, p.rows_per_tile);
@@ -62,17 +85,10 @@ extern "C" int mla_verify_kv4_plan(const mla_verify_desc* d, int32_t num_sms, ml
   // SIMT and few rows: units of (sequence, row tile, chunk), small CTAs, several per SM. tcgen05: one cluster per pair of SMs; the
   // clusters share all tiles equally, at least chunk_tokens / 128 each. That least share only bounds the number of
   // splits that the workspace has room for: the kernel takes the even share of the lengths that it finds.
-  const int64_t slots = simt ? (int64_t)num_sms * 8 : few ? (int64_t)num_sms * 3 : (num_sms / 2 > 0 ? num_sms / 2 : 1);
-  int64_t tiles = d->num_splits > 0 ? cdiv(max_tiles, d->num_splits) : cdiv(cdiv(total, tile) * p.row_tiles, slots);
-  if (few && d->num_splits == 0) {
-    // One wave of CTAs (a sequence's last chunk is half empty on average); the merge reads every split, so at most 128 of
-    // them, and four tiles a CTA but for short calls.
-    const int64_t room = slots - d->num_seqs / 2 > 1 ? slots - d->num_seqs / 2 : 1;
-    const int64_t few_tiles = cdiv(max_tiles, 16) < 4 ? cdiv(max_tiles, 16) : 4, few_splits = cdiv(max_tiles, 128);
-    tiles = cdiv(cdiv(total, tile), room);
-    tiles = tiles > few_tiles ? tiles : few_tiles;
-    tiles = tiles > few_splits ? tiles : few_splits;
-  }
+  const int64_t slots = simt ? (int64_t)num_sms * 8 : few ? few_slots : (num_sms / 2 > 0 ? num_sms / 2 : 1);
+  int64_t tiles = few               ? few_tiles
+                  : d->num_splits > 0 ? cdiv(max_tiles, d->num_splits)
+                                      : cdiv(cdiv(total, tile) * p.row_tiles, slots);
   tiles = tiles < 1 ? 1 : tiles > max_tiles ? max_tiles : tiles;
   if (cdiv(max_tiles, tiles) + 1 > kMaxSplits) tiles = cdiv(max_tiles, kMaxSplits - 1);
   p.chunk_tokens = (int32_t)(tiles * tile);
