@@ -785,7 +785,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) verify_
       };
       for (int n = 1; walk.w < walk.w_end; ++n) {
         // the place of segment n - 2 is free once Q of segment n - 1 is in place: every role has read that one
-        if (!wait_warp(bar(kBarQFull), (n - 1) & 1, abort_flag)) break;
+        // (after all of segment n - 2, which may take longer than other waits do: several times its tiles' time on top)
+        const long long start = clock64(), limit = kTimeoutCycles + (n > 1 ? 32768ll * abs(s_seg[8 * (n & 1) + 5]) : 0);
+        bool ready = mbar_test(bar(kBarQFull), (n - 1) & 1);
+        while (!ready && !*abort_flag && clock64() - start <= limit) ready = mbar_test(bar(kBarQFull), (n - 1) & 1);
+        if (!ready) *abort_flag = 1;
+        if (!__all_sync(0xffffffffu, ready)) break;
         const Segment sg = walk.next(a, lane, lengths_from(a, lane, walk.b0));
         if (lane == 0) {
           put_segment(n, sg, walk.w < walk.w_end);
