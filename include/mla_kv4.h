@@ -75,7 +75,13 @@ int mla_kv4_gather(const void *pool, int64_t num_slots, const int32_t *slots, in
  *   workspace   device, >= mla_verify_kv4_workspace_size bytes, 256-byte aligned.
  * Other arguments, checks and return codes are those of mla_verify_attn. A key row with a NaN
  * scale makes exactly the rows that see it NaN. The result does not depend on which physical
- * slots hold the rows.
+ * slots hold the rows. Scores, maxima, sums and the output's sums are float32 (finite q and RoPE dims of any
+ * size may be used as long as the scores are float32 numbers); each weight and each part's output is rounded to float16 once (2^-11 of the largest
+ * value that the row sees, each), also with out_dtype float32 and with one part.
+ * Give total_tokens_hint where several sequences, or one of more than 128 query rows, are shorter than max_seq_len:
+ * work is shared out by it (mla_verify_kv4_plan). 32 sequences of 301 k positions in all, 128 rows: 96 us with
+ * the hint; without it 251 us when max_seq_len is the longest of them and 1.28 ms when it is 184,320, where the hint
+ * takes 98 us and a workspace of 202 MB instead of 17.
  */
 int mla_verify_attn_kv4(const mla_verify_desc *desc, const void *q, const void *pool, const int32_t *slot_table,
                         const int32_t *seq_lens, const int32_t *tree_sizes, const int32_t *tree_parent, void *out,
@@ -92,7 +98,8 @@ int mla_verify_attn_kv4(const mla_verify_desc *desc, const void *q, const void *
  * the positions of all sequences and row tiles evenly, as the lengths on the device turn out, so a
  * sequence may be cut anywhere, into at most num_splits parts. One sequence of at most 128 query
  * rows is shared evenly whatever its length; otherwise a total_tokens_hint far above the actual
- * lengths leaves pairs without work, and one below them only makes the workspace larger.
+ * lengths (or none, which stands for num_seqs * max_seq_len) leaves pairs without work, and one below them only
+ * makes the workspace larger: it has room for num_splits parts of every row, and the hint divides the parts.
  */
 int mla_verify_kv4_plan(const mla_verify_desc *desc, int32_t num_sms, mla_verify_plan_t *plan);
 int mla_verify_kv4_workspace_size(const mla_verify_desc *desc, size_t *bytes);

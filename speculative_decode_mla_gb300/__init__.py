@@ -452,6 +452,10 @@ def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, 
 
     q: bf16 [B*T, H, 576]; slot_table: int32 [B, stride]; seq_lens: int32 [B]; tree_parent: int32 [B, T];
     tree_sizes: int32 [B] or None. Returns (out [B*T, H, 512], lse [B*T, H]).
+
+    total_tokens_hint: about the sum of seq_lens + T, when it is known. Left out, every sequence counts as max_seq_len long, and
+    a batch of shorter ones can take several times as long (the header has figures). With a max_seq_len far above the
+    lengths the hint costs workspace: kv4_workspace_size() says how much.
     """
     import torch
     dev, i32 = q.get_device(), torch.int32

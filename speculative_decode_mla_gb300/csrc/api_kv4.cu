@@ -21,7 +21,7 @@ int64_t part_o_bytes(const mla_verify_plan_t& p, int64_t rows) {
 
 // One row tile in all: the pairs may share any length evenly, since it has no more splits than there are pairs, and as
 // many at its greatest length. (A captured call of 128 rows with room for 180 Ki positions
-// takes 18 us at 16 Ki, not 50, and 28 at 64 Ki, not 50.)
+// takes 19 us at 16 Ki, not 50, and 29 at 64 Ki, not 50.)
 bool shares_any_length(const mla_verify_desc& d, const mla_verify_plan_t& p, int64_t row_tiles) {
   return p.kernel == 0 && row_tiles == 1 && d.num_splits == 0;
 }

@@ -3,8 +3,8 @@
 // Both kernels are bound by memory: append reads 1152 + 4 bytes and writes 416 per row, gather the
 // other way round. One warp takes a row at a time, kRowsPerWarp rows in flight, so every access is a run
 // of 128 to 512 consecutive bytes and a warp has its loads out before it waits on one. Append and then gather
-// of 65,536 rows (one in seven skipped): 33.9 us, 83% of the copy rate; gather of 184,320: 46.8 us, 92%. Append was at
-// 71% of the issue slots with two true divisions a row and lane, so it does without them (see below).
+// of 65,536 rows (one in seven skipped): 34 us, 82% of the copy rate; gather of 184,320: 46.8 us, 92%. Append, whose issue
+// slots are 61% in use, does without true divisions (see below): with two a row and lane the pair took 35.2 us, then 33.5.
 #include "kv4.cuh"
 
 namespace mla {

@@ -11,11 +11,13 @@
 //   16 dims, in Q's order too.  V operand: 8 bytes, the dims [16g, 16g + 16), of the keys 2t, 2t + 1, 2t + 8, 2t + 9; column
 //   g of MMA j is dim 16g + j, so a thread ends with 32 dims in a row of its two rows.
 // Codes lie as 128-byte lines of two keys, 16-byte chunk c at c ^ 2 (line % 4): conflict-free for both reads.
-// What bounds it: the chain of a tile (copies, S, exchange, softmax, PV: about 2700 cycles for a CTA alone, 1100 a CTA
-// with three on an SM) and the issue slots (44% of them in use); tensor pipe 29%, DRAM 19%. MMAs of one key after another
-// instead of interleaved took 5 to 8% longer, two CTAs on an SM without spills 25% (here: 8 bytes spilled).
-//   16 rows: 32 sequences of 8192 positions 64 us, 1024 of 300 122 us, 4096 of 300 335 us (8 rows), merge included
-// Rounding as in verify_kv4_tc.cu: Q's rows and the keys scaled by powers of two (kv4.cuh), P = 2^(s - m + 7) in fp16, l from unrounded weights.
+// What bounds it: the chain of a tile (copies, S, exchange, softmax, PV: about 2700 cycles for a CTA alone, 5000 with three on
+// an SM, 1870 a tile of the SM) and the issue slots (48% of the active cycles, 32 sequences of 8192 positions); tensor pipe
+// 29%, DRAM 26%. MMAs of one key after another instead of interleaved took 5 to 8% longer, two CTAs on an SM without spills
+// 25% (here: 8 bytes spilled).
+//   16 rows: 32 sequences of 8192 positions 64 us, 1024 of 300 123 us, 4096 of 300 433 us (8 rows: 335), merge included
+// Rounding as in verify_kv4_tc.cu: Q's rows and the keys scaled by powers of two (kv4.cuh), P = 2^(s - m + 7) in fp16, l from
+// unrounded weights.
 #include <atomic>
 
 #include "kv4.cuh"

@@ -37,16 +37,17 @@
 // TMEM (512 columns): O [0, 256), two S buffers [256, 384), Q's dims 0..255 [384, 512) (both lane halves hold the
 // CTA's 64 rows); Q's dims 256..511 and RoPE dims are in shared memory.
 //
-// What bounds it: the L1 data path. Per tile and SM its counters show (256 rows x 180 Ki positions) 2780 wavefronts of
+// What bounds it: the L1 data path. Per tile and SM its counters show (256 rows x 180 Ki positions) 2830 wavefronts of
 // loads and stores (152 KB of K, V, RoPE dims and P stored: 1220 at least, 1440 with the barriers; the gathered rows,
-// 40 KB, in and out to registers: 1120) and 1660 of MMA operands (S: 72 KB of K, 40 of Q; PV: 64 of V, P twice), together
-// 97% of the SM's active cycles; a tile takes about 4050, the tensor cores need 2200 of them (64 rows on each SM are half
+// 40 KB, in and out to registers: 1160) and 1660 of MMA operands (S: 72 KB of K, 40 of Q; PV: 64 of V, P twice), together
+// as many as the SM has active cycles; the tensor cores need 2200 a tile (64 rows on each SM are half
 // their rate). A segment costs about three tiles more (O out, Q in, and the
-// first tile's K and V before the first PV), launch and merge about 10 us. The gather does not spill at 72
-// registers; at 64, with 24 bytes spilled, 4096 rows x 128 Ki took 918 us instead of 867.
-//   rows x positions (sequences): 64 x 1 Ki 13.4 us, 128 x 64 Ki 27.7, 256 x 180 Ki 95, 128 x 301 k (32) 95,
-//   64 x 250 k (61) 87, 4096 x 128 Ki 867 (1.35 PFLOP/s); merge included
-// One unit (sequence, row tile, chunk) a cluster, without the shares: 12.7, 28.5, 95, 118, 105, 938.
+// first tile's K and V before the first PV), launch and merge about 10 us. 36 bytes are spilled in all (none before the
+// maximum was taken away ahead of the product, at the same speed); the gather at 64 registers instead of 72, with 24 bytes
+// spilled there, took 918 us for 4096 rows x 128 Ki instead of 867.
+//   rows x positions (sequences): 64 x 1 Ki 13.3 us, 128 x 64 Ki 27.8, 256 x 180 Ki 94, 128 x 301 k (32) 93,
+//   64 x 250 k (61) 86, 4096 x 128 Ki 859 (1.36 PFLOP/s); merge included
+// One unit (sequence, row tile, chunk) a cluster, without the shares: 12.7, 28.5, 95, 118, 105, 938 (95.5 us then for 180 Ki).
 //
 // Positions past a sequence's end read slot 0's row and are masked; values whose scale is NaN are 0
 // in V (their K is NaN, so every row that sees the key is NaN through its weight, and no other).
@@ -94,7 +95,7 @@ constexpr int kQTmemDims = 256;
 static_assert(2 * kVHalfBytes >= kCtaRows * kQTmemDims * 2, "half of Q passes through V's place");
 constexpr int kOutRow = kDLatent * 2 + 16;  // a row of the output on its way out: 8 rows' chunks lie in different banks
 static_assert(kCtaRows * kOutRow <= kKSlots * kKSlotBytes, "output rows");
-constexpr int kPrefetchTiles = 3;  // of the next segment, to L2: 4096 sequences of 300 positions took 911 us with 1, 878 with 3
+constexpr int kPrefetchTiles = 3;  // of the next segment, to L2: 4096 sequences of 300 positions, 16 rows, took 911 us with 1, 878 with 3 then
 constexpr float kPBias = 7.f;
 
 constexpr int kBarKFull = 0, kBarKEmpty = kKSlots, kBarVFull = 2 * kKSlots /*2*/, kBarVEmpty = kBarVFull + 2 /*2*/,
