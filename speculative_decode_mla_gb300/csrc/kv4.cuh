@@ -28,10 +28,10 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
 // 2^12, fp16 holds multiples of 2^-24 of that many bits), so that the RoPE part of the scores, which lie in the same sum, has
 // room: a query row is scaled by a power of two to [2^7, 2^8) at its largest, its RoPE dims in bf16 by 2^-kKeyShift more, below 2^-6,
 // and 64 products with any finite bf16 keys then stay within fp32. Latent dims of Q are exact in fp16 down to 2^-24 of the row's
-// largest and off by at most 2^-32 of it below that, less than the fp32 sum itself.
+// largest and off by at most 2^-32 of it below that (the fp32 sum is off by 2^-24 of that largest one's product).
 constexpr int kKeyShift = 14;
 // k of the factor 2^k for a query row, given its largest magnitude as bf16 bits: rows with infinities or NaN stay as they are, and
-// the two limits keep the factors and their inverses normal fp32 numbers (a row of 2^119 and more gets up to [2^14, 2^15)).
+// the two limits keep the factors and their inverses normal fp32 numbers (a row of 2^121 and more gets up to [2^14, 2^15)).
 __device__ __forceinline__ int query_shift(uint32_t top) {
   const int e = (int)(top >> 7);
   return e == 255 ? 0 : max(-113, min(110, 134 - e));
