@@ -345,3 +345,63 @@ def slot_map_build(seq_lens, new_lens, held_lens, page_size: int, num_pages: int
             slot_map[cu[-1] + t - L] = slot
         cu.append(cu[-1] + n)
     return (block, table, slot_map, np.array(cu, np.int32), np.array([w[3] for w in wish], np.int32), left, found)
+
+
+# ---- a layer's norms and rotations, and prompt attention, as include/mla_prompt.h defines them ----
+def turn(x: np.ndarray, cos_sin: np.ndarray, halves: bool) -> np.ndarray:
+    """Vectors [n, ..., 64] (float64), token i turned by cos_sin[i] = 32 cosines, 32 sines."""
+    c = cos_sin[:, :32].astype(np.float64).reshape((-1,) + (1,) * (x.ndim - 2) + (32,))
+    s = cos_sin[:, 32:].astype(np.float64).reshape(c.shape)
+    a = np.arange(32) if halves else 2 * np.arange(32)
+    b = a + (32 if halves else 1)
+    y = np.empty_like(x)
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., b] * c + x[..., a] * s
+    return y
+
+
+def norm(x: np.ndarray, weight: Optional[np.ndarray], eps: float) -> np.ndarray:
+    """weight * x / sqrt(mean(x^2) + eps) over the last axis (x itself without a weight)."""
+    return x if weight is None else weight * x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+
+
+def rope_rows(rows: np.ndarray, cos_sin: np.ndarray, weight: Optional[np.ndarray], eps: float, halves: bool) -> np.ndarray:
+    """rows [n, 576] in float64: the latent dims normalised, the RoPE dims turned."""
+    return np.concatenate([norm(rows[:, :512], weight, eps), turn(rows[:, 512:], cos_sin, halves)], 1)
+
+
+def rope_heads(q: np.ndarray, cos_sin: np.ndarray, weight: Optional[np.ndarray], eps: float, halves: bool) -> np.ndarray:
+    """Query heads [n, heads, d] in float64: normalised, their last 64 dims turned."""
+    z = norm(q, weight, eps)
+    return np.concatenate([z[..., :-64], turn(z[..., -64:], cos_sin, halves)], -1)
+
+
+def prompt_attn(q, k, k_rope, v, cu_q, cu_k, *, causal: bool, scale: float):
+    """(out, lse, spread, size) in float64: spread = sum of weights times |values|, size = the largest sum of |q||k| among
+    the keys that a row sees, times scale (what a rounding error of the scores is relative to). Rows outside the
+    sequences stay NaN; a row without keys has out 0, lse -inf."""
+    heads, group = q.shape[1], q.shape[1] // k.shape[1]
+    out = np.full((q.shape[0], heads, v.shape[2]), np.nan)
+    spread, lse, size = out.copy(), np.full((q.shape[0], heads), np.nan), np.full((q.shape[0], heads), np.nan)
+    for b in range(len(cu_q) - 1):
+        m, n = int(cu_q[b + 1] - cu_q[b]), int(cu_k[b + 1] - cu_k[b])
+        if m == 0:
+            continue
+        at = slice(int(cu_k[b]), int(cu_k[b]) + n)
+        for h in range(heads):
+            key = np.concatenate([k[at, h // group], k_rope[at]], 1)
+            val = v[at, h // group]
+            rows = q[int(cu_q[b]):int(cu_q[b]) + m, h]
+            with np.errstate(invalid="ignore", over="ignore"):
+                s, mag = rows @ key.T * scale, np.abs(rows) @ np.abs(key).T * scale
+                for i in range(m):
+                    r, vis = int(cu_q[b]) + i, max(0, min(n, i + n - m + 1)) if causal else n
+                    if vis == 0:
+                        out[r, h], spread[r, h], lse[r, h], size[r, h] = 0.0, 0.0, -np.inf, 0.0
+                        continue
+                    top = s[i, :vis].max()
+                    w = np.exp(s[i, :vis] - top)
+                    z = w.sum()
+                    out[r, h], spread[r, h] = w / z @ val[:vis], w / z @ np.abs(val[:vis])
+                    lse[r, h], size[r, h] = top + np.log(z), mag[i, :vis].max()
+    return out, lse, spread, size

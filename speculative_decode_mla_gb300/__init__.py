@@ -13,6 +13,11 @@ The same over a pool held in 4 bits (``include/mla_kv4.h``), with the step's slo
     slot_map, cu_new, held, left = slot_map_build(seq_lens, new_lens, free_pages, free_count, slot_table, ...)
     kv4_append(pool4, rows, slot_map)
     out, lse = verify_kv4(q, pool4, slot_table, seq_lens, tree_parent, max_seq_len=L)
+
+What comes before it (``include/mla_prompt.h``): a layer's norms, rotations and rows into either pool, and a prompt's attention:
+
+    rows_out, q_out = rope_append(pool, rows, slot_map, positions, cos_sin, weight=w, q=q)
+    out, lse = prompt_attn(q_out, k_nope, rows_out[:, 512:], v, cu, max_q_len=L)
 """
 from __future__ import annotations
 
@@ -30,6 +35,9 @@ MLA_OK = 0
 MLA_DTYPE_BF16, MLA_DTYPE_F32, MLA_DTYPE_F16 = 0, 1, 2
 MLA_FLAG_DEBUG_CHECKS, MLA_FLAG_SIMT, MLA_FLAG_PREFIX_STABLE = 1, 2, 4
 CHECK_BAD_SLOT, CHECK_BAD_PARENT, CHECK_BAD_LENGTH, CHECK_TIMEOUT, CHECK_NO_PAGES = 1, 2, 4, 8, 16
+CHECK_BAD_POSITION = 32
+MLA_POOL_NONE, MLA_POOL_BF16, MLA_POOL_KV4 = 0, 1, 2
+MLA_ROPE_ADJACENT, MLA_ROPE_HALVES = 0, 1
 D_LATENT, D_ROPE = 512, 64
 KV4_ROW_BYTES = 416  # a row of the 4-bit pool
 DEFAULT_SCALE = 1.0 / math.sqrt(192.0)
@@ -50,6 +58,30 @@ class Plan(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("num_splits", ctypes.c_int32), ("chunk_tokens", ctypes.c_int32),
                 ("row_tiles", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("ctas", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("num_slots", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q_out_token_stride", ctypes.c_int64), ("q_out_head_stride", ctypes.c_int64),
+                ("pool_format", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("num_positions", ctypes.c_int32), ("pairs", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class PromptDesc(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32), ("max_k_len", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("num_splits", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("num_q", ctypes.c_int64), ("num_k", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("k_rope_token_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64)]
+
+
+class PromptPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("num_splits", ctypes.c_int32), ("rows_per_unit", ctypes.c_int32),
+                ("listed", ctypes.c_int32), ("units", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
 
 
 class MLAError(RuntimeError):
@@ -89,7 +121,12 @@ def load_library(path: str = LIB_PATH):
     lib.mla_verify_kv4_plan.argtypes = [ctypes.POINTER(Desc), i32, ctypes.POINTER(Plan)]
     lib.mla_verify_kv4_workspace_size.argtypes = [ctypes.POINTER(Desc), ctypes.POINTER(ctypes.c_size_t)]
     lib.mla_verify_attn_kv4.argtypes = [ctypes.POINTER(Desc), P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P]
-    for f in ("mla_verify_plan", "mla_verify_workspace_size", "mla_verify_attn", "mla_verify_attn_partials",
+    lib.mla_rope_append.argtypes = [ctypes.POINTER(RopeDesc), P, P, P, P, P, P, P, P, P, P, i32, P, P]
+    lib.mla_prompt_plan.argtypes = [ctypes.POINTER(PromptDesc), i32, ctypes.POINTER(PromptPlan)]
+    lib.mla_prompt_workspace_size.argtypes = [ctypes.POINTER(PromptDesc), ctypes.POINTER(ctypes.c_size_t)]
+    lib.mla_prompt_attn.argtypes = [ctypes.POINTER(PromptDesc), P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P, P]
+    for f in ("mla_rope_append", "mla_prompt_plan", "mla_prompt_workspace_size", "mla_prompt_attn",
+              "mla_verify_plan", "mla_verify_workspace_size", "mla_verify_attn", "mla_verify_attn_partials",
               "mla_verify_attn_hybrid", "mla_verify_attn_ragged",
               "mla_verify_combine", "mla_fill_normal_bf16", "mla_tree_kv_append", "mla_tree_accept_commit",
               "mla_kv_compact", "mla_slot_map_build", "mla_kv4_append", "mla_kv4_gather", "mla_verify_kv4_plan",
@@ -494,6 +531,166 @@ def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, 
             _ptr_or_none(tree_sizes), tree_parent.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
             workspace.numel(), _ptr_or_none(dev_status), raw)
     _check(rc, "mla_verify_attn_kv4")
+    return out, lse
+
+
+def _check_heads(name: str, t, shape, device: int):
+    """A bf16 tensor [rows, heads, dims] of this shape (None: any extent) on `device` with contiguous dims, or ValueError."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.get_device() != device:
+        raise ValueError(f"{name} must be torch.bfloat16 on cuda:{device}: got {t.dtype} on {t.device}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}: got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the dims of a row of {name} must be contiguous")
+
+
+def rope_append(pool, rows, slot_map, positions, cos_sin, *, weight=None, eps: float = 1e-6, rows_out=None,
+                want_rows: bool = True, q=None, q_weight=None, q_out=None, halves: bool = False, debug: bool = False,
+                dev_status=None, stream=None):
+    """Norm and rotate a layer's latent rows and query heads, and put the rows into the pool (``include/mla_prompt.h``).
+
+    pool: bf16 [slots, 576] or the 4-bit pool uint8 [slots, 416], written in place at slot_map (int32 [n], -1: not into the
+    pool), or None; rows: bf16 [n, 576] (may be strided, dims contiguous), or None for the queries alone; positions: int32 [n]
+    (-1: a padding row); cos_sin: float32 [positions, 64], cosines then sines; weight: bf16 [512], the norm of the latent dims, or
+    None. q: bf16 [n, heads, d] (may be strided), its last 64 dims rotated; q_weight: bf16 [d], a norm of each head, or None;
+    halves: pairs k, k + 32 instead of 2k, 2k + 1. rows_out may be rows and q_out may be q: in place.
+    Returns (rows_out [n, 576], q_out): new tensors where none were passed in; rows_out is None with want_rows=False, or without
+    rows, and q_out without q. (Rows of new tensors whose position is -1 hold nothing.)
+    """
+    import torch
+    dev, n, bf16 = positions.get_device(), positions.shape[0], torch.bfloat16
+    _check_tensor("positions", positions, torch.int32, (n,), dev)
+    _check_tensor("cos_sin", cos_sin, torch.float32, (cos_sin.shape[0], D_ROPE), dev)
+    d = RopeDesc(num_rows=n, num_positions=cos_sin.shape[0], pairs=MLA_ROPE_HALVES if halves else MLA_ROPE_ADJACENT,
+                 eps=float(eps))
+    if dev_status is not None:
+        _check_tensor("dev_status", dev_status, torch.int32, (1,), dev)
+    if rows is not None:
+        _check_heads("rows", rows, (n, D_LATENT + D_ROPE), dev)
+        d.row_stride = rows.stride(0) if n > 1 else D_LATENT + D_ROPE
+        if weight is not None:
+            _check_tensor("weight", weight, bf16, (D_LATENT,), dev)
+        if pool is not None:
+            if pool.dtype is bf16:
+                _check_tensor("pool", pool, bf16, (pool.shape[0], D_LATENT + D_ROPE), dev)
+                d.pool_format = MLA_POOL_BF16
+            else:
+                _check_tensor("pool", pool, torch.uint8, (pool.shape[0], KV4_ROW_BYTES), dev)
+                d.pool_format = MLA_POOL_KV4
+            if slot_map is None:
+                raise ValueError("a pool needs a slot_map")
+            _check_tensor("slot_map", slot_map, torch.int32, (n,), dev)
+            d.num_slots = pool.shape[0]
+        elif slot_map is not None:
+            raise ValueError("a slot_map needs a pool")
+        if rows_out is not None:
+            _check_tensor("rows_out", rows_out, bf16, (n, D_LATENT + D_ROPE), dev)
+        elif pool is None and not want_rows:
+            raise ValueError("rows need a pool or rows_out")
+    elif pool is not None or slot_map is not None or weight is not None or rows_out is not None:
+        raise ValueError("pool, slot_map, weight and rows_out need rows")
+    elif q is None:
+        raise ValueError("rows or q is needed")
+    if q is not None:
+        _check_heads("q", q, (n, None, None), dev)
+        heads, dim = q.shape[1], q.shape[2]
+        d.num_heads, d.head_dim = heads, dim
+        d.q_token_stride, d.q_head_stride = q.stride(0) if n > 1 else heads * dim, q.stride(1) if heads > 1 else dim
+        if q_weight is not None:
+            _check_tensor("q_weight", q_weight, bf16, (dim,), dev)
+        if q_out is not None:
+            _check_heads("q_out", q_out, (n, heads, dim), dev)
+            d.q_out_token_stride = q_out.stride(0) if n > 1 else heads * dim
+            d.q_out_head_stride = q_out.stride(1) if heads > 1 else dim
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    raw, here = _on(dev, stream)
+    with here:
+        if rows is not None and rows_out is None and want_rows:
+            rows_out = torch.empty((n, D_LATENT + D_ROPE), dtype=bf16, device=positions.device)
+        if q is not None and q_out is None:
+            q_out = torch.empty(tuple(q.shape), dtype=bf16, device=positions.device)
+            d.q_out_token_stride, d.q_out_head_stride = heads * dim, dim
+        rc = load_library().mla_rope_append(
+            ctypes.byref(d), _ptr_or_none(rows), _ptr_or_none(weight), _ptr_or_none(q), _ptr_or_none(q_weight),
+            positions.data_ptr(), cos_sin.data_ptr(), _ptr_or_none(slot_map), _ptr_or_none(pool), _ptr_or_none(rows_out),
+            _ptr_or_none(q_out), int(debug), _ptr_or_none(dev_status), raw)
+    _check(rc, "mla_rope_append")
+    return rows_out, q_out
+
+
+def prompt_plan(desc: PromptDesc, num_sms: int) -> PromptPlan:
+    p = PromptPlan()
+    _check(load_library().mla_prompt_plan(ctypes.byref(desc), int(num_sms), ctypes.byref(p)), "mla_prompt_plan")
+    return p
+
+
+def prompt_workspace_size(desc: PromptDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().mla_prompt_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "mla_prompt_workspace_size")
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=256)
+def _prompt_desc(device_index, *fields):
+    """(desc, workspace bytes) of a call's shapes: a pure function of them and of the device's SM count."""
+    desc = PromptDesc(*fields)
+    return desc, prompt_workspace_size(desc)
+
+
+def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_len: Optional[int] = None,
+                causal: bool = True, softmax_scale: float = DEFAULT_SCALE, out_dtype: int = MLA_DTYPE_BF16,
+                flags: Optional[int] = None, num_splits: int = 0, out=None, lse=None, workspace=None, dev_status=None,
+                stream=None):
+    """Causal attention of packed prompts, or of their next chunks (``include/mla_prompt.h``).
+
+    q: bf16 [num_q, H, 192]; k_nope, v: bf16 [num_k, Hk, 128], H a multiple of Hk; k_rope: bf16 [num_k, 64], shared by the heads
+    (all may be strided in multiples of 8 elements, dims contiguous); cu_q, cu_k: int32 [B + 1], where the sequences' queries and
+    keys begin and end (cu_k None: the same as cu_q). A sequence's queries are the last of its places. max_q_len, max_k_len: upper bounds
+    of their lengths (max_k_len None: max_q_len). Returns (out [num_q, H, 128], lse [num_q, H]); rows outside the sequences are left
+    as they were.
+    """
+    import torch
+    dev, i32, bf16 = q.get_device(), torch.int32, torch.bfloat16
+    _check_heads("q", q, (None, None, 192), dev)
+    nq, heads = q.shape[0], q.shape[1]
+    _check_heads("k_nope", k_nope, (None, None, 128), dev)
+    nk, hk = k_nope.shape[0], k_nope.shape[1]
+    _check_heads("k_rope", k_rope, (nk, D_ROPE), dev)
+    _check_heads("v", v, (nk, hk, 128), dev)
+    if cu_k is None:
+        cu_k = cu_q
+    B = cu_q.shape[0] - 1
+    _check_tensor("cu_q", cu_q, i32, (B + 1,), dev)
+    _check_tensor("cu_k", cu_k, i32, (B + 1,), dev)
+    if dev_status is not None:
+        _check_tensor("dev_status", dev_status, i32, (1,), dev)
+    out_type = bf16 if out_dtype == MLA_DTYPE_BF16 else torch.float32
+    raw, here = _on(dev, stream)
+    with here:
+        # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
+        desc, need = _prompt_desc(
+            dev, B, heads, hk, int(max_q_len), int(max_q_len if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
+            int(DEFAULT_FLAGS if flags is None else flags), int(num_splits), float(softmax_scale), nq, nk, q.stride(0), q.stride(1),
+            k_nope.stride(0), k_nope.stride(1), k_rope.stride(0), v.stride(0), v.stride(1))
+        if out is None:
+            out = torch.empty((nq, heads, 128), device=q.device, dtype=out_type)
+        else:
+            _check_tensor("out", out, out_type, (nq, heads, 128), dev)
+        if lse is None:
+            lse = torch.empty((nq, heads), device=q.device, dtype=torch.float32)
+        else:
+            _check_tensor("lse", lse, torch.float32, (nq, heads), dev)
+        if workspace is not None:
+            _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+        elif need:
+            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        rc = load_library().mla_prompt_attn(
+            ctypes.byref(desc), q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
+            cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr_or_none(workspace),
+            0 if workspace is None else workspace.numel(), _ptr_or_none(dev_status), raw)
+    _check(rc, "mla_prompt_attn")
     return out, lse
 
 

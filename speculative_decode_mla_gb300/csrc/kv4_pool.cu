@@ -23,56 +23,6 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// The e4m3 scale of a block: max|x| / 6, the exact quotient rounded to nearest even and at most
-// 448; NaN (0x7f) when the block holds a NaN or an infinity. `top`: the largest bf16 magnitude as bits.
-// top times fp32's 1/6 serves as the quotient: fp32's 1/6 is off by 2^-25 of itself. If top / 6 is a midpoint m of e4m3
-// (at most 5 significant bits), the product lies within m * 2^-25 of m, under half an ulp, and rounds to m; if not, it
-// is off every midpoint by 2^-8 of its size (top has 8 significant bits, 6 m has 7), so rounding twice is harmless.
-__device__ __forceinline__ uint32_t block_scale(uint32_t top) {
-  uint16_t s;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(__uint_as_float(top << 16) * (1.f / 6.f)));
-  return top >= 0x7f80u ? 0x7fu : s & 0xffu;
-}
-
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-// Codes of eight values (four words of bf16 pairs) under the scale byte. y = x / s is taken as x * r, r = 1 / s within
-// 2^-23 of itself, and rounded to a multiple of 2^-11 by adding and taking away 1.5 * 2^12: a quotient on one
-// of e2m1's midpoints (0.25 .. 5) comes out exactly on it, and any other stays off it, since x has 8
-// significant bits and s * midpoint at most 7, so they differ by 2^-8 of their size or not at all.
-__device__ __forceinline__ uint32_t block_codes(const uint4& w, uint32_t scale) {
-  const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(scale) & 0xffffu)));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));  // (s is 0, NaN or a normal fp32 number)
-  const uint64_t rr = pack2(r, r), magic = pack2(6144.f, 6144.f), minus = pack2(-6144.f, -6144.f);
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t v = pack2(bf16_lo(x[i]), bf16_hi(x[i]));
-    asm("{\n.reg .b64 y;\n.reg .f32 lo, hi;\n.reg .b8 d;\n"
-        "fma.rn.f32x2 y, %1, %2, %3;\nadd.rn.f32x2 y, y, %4;\nmov.b64 {lo, hi}, y;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 d, hi, lo;\nmov.b32 %0, {d, 0, 0, 0};\n}"
-        : "=r"(c[i])
-        : "l"(v), "l"(rr), "l"(magic), "l"(minus));
-    const uint32_t sign = x[i] & 0x80008000u;  // a negative value that rounds to zero has lost its sign by now
-    c[i] |= (sign >> 12) | (sign >> 24);       // (only the low byte is used)
-  }
-  const uint32_t out = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-  return s > 0.f ? out : 0u;  // (scale 0 or NaN: codes 0)
-}
-
-__device__ __forceinline__ uint32_t top_of(const uint4& w) {
-  uint32_t t = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-  return max(t & 0xffffu, t >> 16);
-}
-
 // Lane l quantises dims [8l, 8l + 8) and [256 + 8l, 256 + 8l + 8) of its warp's row: two lanes share a block.
 __global__ void __launch_bounds__(kPoolThreads) kv4_append_kernel(uint8_t* __restrict__ pool, int64_t num_slots,
                                                                   const __nv_bfloat16* __restrict__ rows,
