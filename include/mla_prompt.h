@@ -95,7 +95,7 @@ typedef struct mla_prompt_desc {
   int32_t causal;          /* 1: query i sees keys up to its own place; 0: all keys of its sequence */
   int32_t out_dtype;       /* MLA_DTYPE_BF16 or MLA_DTYPE_F32 */
   int32_t flags;           /* MLA_FLAG_DEBUG_CHECKS, MLA_FLAG_SIMT */
-  int32_t num_splits;      /* 0: planner decides; > 0: cut every row's keys into this many parts (at most 1024) */
+  int32_t num_ctas;        /* 0: planner decides; > 0: the work is shared out evenly over this many CTAs (at most 1024) */
   float softmax_scale;     /* finite and > 0 */
   int64_t num_q, num_k;    /* rows of q (and out, lse), and of k_nope, k_rope and v; 0 .. 2^30 */
   int64_t q_token_stride, q_head_stride;  /* all strides: multiples of 8, from 8 to 2^38 */
@@ -107,10 +107,12 @@ typedef struct mla_prompt_desc {
 /* The launch plan chosen for a desc (for introspection and tests). */
 typedef struct mla_prompt_plan_t {
   int32_t kernel;          /* 0: tcgen05 kernel, 1: SIMT reference kernel */
-  int32_t num_splits;      /* parts of every row's keys */
-  int32_t rows_per_unit;   /* query rows of one head that a CTA works on at a time */
-  int32_t listed;          /* 1: a first kernel sorts the batch's units, longest first */
-  int64_t units;           /* an upper bound of the units, which is what is launched */
+  int32_t rows_per_unit;   /* rows (query and head) that a CTA works on at a time: 256, or 128 when no sequence has more */
+  int32_t pack;            /* query heads of one key head that share a unit's rows: H / num_kv_heads, or 1 */
+  int32_t shared;          /* 1: the CTAs share all tiles of keys evenly, and parts of a unit are merged; 0: whole units */
+  int32_t listed;          /* 1: a first kernel lists the batch's units */
+  int32_t reserved;
+  int64_t ctas;            /* CTAs launched: with shared 0, an upper bound of the units */
   int64_t workspace_bytes; /* 0 when none is needed */
 } mla_prompt_plan_t;
 
@@ -140,7 +142,7 @@ int mla_prompt_workspace_size(const mla_prompt_desc *desc, size_t *bytes);
  *   workspace  device, >= mla_prompt_workspace_size bytes, 256-byte aligned (NULL where that is 0).
  *   dev_status as for mla_verify_attn.
  * Weights are rounded to bf16 for the product with V; scores, maxima, sums and outputs are float32, and
- * the parts of a row are merged in float32. out, lse and workspace may overlap nothing else of the call.
+ * where a row's keys are cut into parts (calls with few units, by the lengths on the device) these are merged in float32. out, lse and workspace may overlap nothing else of the call.
  */
 int mla_prompt_attn(const mla_prompt_desc *desc, const void *q, const void *k_nope, const void *k_rope, const void *v,
                     const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse, void *workspace,

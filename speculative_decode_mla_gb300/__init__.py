@@ -71,7 +71,7 @@ class RopeDesc(ctypes.Structure):
 class PromptDesc(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("max_q_len", ctypes.c_int32), ("max_k_len", ctypes.c_int32), ("causal", ctypes.c_int32),
-                ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("num_splits", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("num_ctas", ctypes.c_int32),
                 ("softmax_scale", ctypes.c_float), ("num_q", ctypes.c_int64), ("num_k", ctypes.c_int64),
                 ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
                 ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
@@ -80,8 +80,9 @@ class PromptDesc(ctypes.Structure):
 
 
 class PromptPlan(ctypes.Structure):
-    _fields_ = [("kernel", ctypes.c_int32), ("num_splits", ctypes.c_int32), ("rows_per_unit", ctypes.c_int32),
-                ("listed", ctypes.c_int32), ("units", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
+    _fields_ = [("kernel", ctypes.c_int32), ("rows_per_unit", ctypes.c_int32), ("pack", ctypes.c_int32),
+                ("shared", ctypes.c_int32), ("listed", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("ctas", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
 
 
 class MLAError(RuntimeError):
@@ -641,7 +642,7 @@ def _prompt_desc(device_index, *fields):
 
 def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_len: Optional[int] = None,
                 causal: bool = True, softmax_scale: float = DEFAULT_SCALE, out_dtype: int = MLA_DTYPE_BF16,
-                flags: Optional[int] = None, num_splits: int = 0, out=None, lse=None, workspace=None, dev_status=None,
+                flags: Optional[int] = None, num_ctas: int = 0, out=None, lse=None, workspace=None, dev_status=None,
                 stream=None):
     """Causal attention of packed prompts, or of their next chunks (``include/mla_prompt.h``).
 
@@ -672,7 +673,7 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
         # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
         desc, need = _prompt_desc(
             dev, B, heads, hk, int(max_q_len), int(max_q_len if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
-            int(DEFAULT_FLAGS if flags is None else flags), int(num_splits), float(softmax_scale), nq, nk, q.stride(0), q.stride(1),
+            int(DEFAULT_FLAGS if flags is None else flags), int(num_ctas), float(softmax_scale), nq, nk, q.stride(0), q.stride(1),
             k_nope.stride(0), k_nope.stride(1), k_rope.stride(0), v.stride(0), v.stride(1))
         if out is None:
             out = torch.empty((nq, heads, 128), device=q.device, dtype=out_type)

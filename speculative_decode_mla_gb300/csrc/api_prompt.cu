@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t kMaxRows = 1ll << 30;
 constexpr int64_t kGroupBytes = 48ll << 20;  // keys and values of the heads that run at a time, in L2
+constexpr int64_t kSharedUnits = 4;          // calls with fewer units than so many times the SMs share their tiles evenly
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -18,11 +19,11 @@ int check_prompt(const mla_prompt_desc* d) {
   if (!d || d->num_seqs < 1 || d->num_heads < 1 || d->num_kv_heads < 1 || d->num_heads % d->num_kv_heads != 0)
     return MLA_ERR_INVALID_ARGUMENT;
   if (d->max_q_len < 0 || d->max_k_len < 0 || d->num_q < 0 || d->num_k < 0) return MLA_ERR_INVALID_ARGUMENT;
-  if (d->num_q > kMaxRows || d->num_k > kMaxRows || d->num_q * d->num_heads > (1ll << 40)) return MLA_ERR_UNSUPPORTED;
+  if (d->num_q > kMaxRows || d->num_k > kMaxRows || d->num_q * d->num_heads > 0x7fffff00ll) return MLA_ERR_UNSUPPORTED;
   if (d->causal != 0 && d->causal != 1) return MLA_ERR_INVALID_ARGUMENT;
   if (d->out_dtype != MLA_DTYPE_BF16 && d->out_dtype != MLA_DTYPE_F32) return MLA_ERR_INVALID_ARGUMENT;
   if (d->flags & ~(MLA_FLAG_DEBUG_CHECKS | MLA_FLAG_SIMT)) return MLA_ERR_INVALID_ARGUMENT;
-  if (d->num_splits < 0 || d->num_splits > kMaxPromptSplits) return MLA_ERR_INVALID_ARGUMENT;
+  if (d->num_ctas < 0 || d->num_ctas > kMaxPromptCtas) return MLA_ERR_INVALID_ARGUMENT;
   if (!isfinite(d->softmax_scale) || !(d->softmax_scale > 0.f)) return MLA_ERR_INVALID_ARGUMENT;
   // the stride of a dim with one element is not used
   if ((d->num_q > 1 && !good_stride(d->q_token_stride)) || (d->num_heads > 1 && !good_stride(d->q_head_stride)))
@@ -33,11 +34,18 @@ int check_prompt(const mla_prompt_desc* d) {
   return MLA_OK;
 }
 
+// Query heads of a key head that share a unit's rows: all of them, if the tile can be divided among them.
+int32_t pack_of(const mla_prompt_desc& d) {
+  const int32_t group = d.num_heads / d.num_kv_heads;
+  return group <= kPromptTile && (group & (group - 1)) == 0 ? group : 1;
+}
+int64_t longest_q(const mla_prompt_desc& d) { return d.max_q_len < d.num_q ? d.max_q_len : d.num_q; }
 // Row tiles of all sequences, at most.
 int64_t entries_of(const mla_prompt_desc& d, int64_t rows) {
-  const int64_t most = d.max_q_len < d.num_q ? d.max_q_len : d.num_q, a = d.num_seqs * cdiv(most, rows), b = d.num_q / rows + d.num_seqs;
+  const int64_t pack = pack_of(d), a = d.num_seqs * cdiv(longest_q(d) * pack, rows), b = d.num_q * pack / rows + d.num_seqs;
   return a < b ? a : b;
 }
+int64_t pad(int64_t bytes) { return cdiv(bytes, 256) * 256; }
 
 }  // namespace
 }  // namespace mla
@@ -50,42 +58,25 @@ extern "C" int mla_prompt_plan(const mla_prompt_desc* d, int32_t num_sms, mla_pr
   if (!plan || num_sms < 1) return MLA_ERR_INVALID_ARGUMENT;
   mla_prompt_plan_t p;
   memset(&p, 0, sizeof p);
-  const int64_t rows = d->num_q * d->num_heads;
   const int64_t most_k = d->max_k_len < d->num_k ? d->max_k_len : d->num_k, tiles = cdiv(most_k, kPromptTile);
+  p.pack = pack_of(*d);
   if (d->flags & MLA_FLAG_SIMT) {
     p.kernel = 1;
-    p.rows_per_unit = 1;
-    p.num_splits = d->num_splits > 0 ? d->num_splits : 1;
-    p.units = rows * p.num_splits;
+    p.rows_per_unit = p.pack = 1;
+    p.ctas = d->num_q * d->num_heads;
   } else {
-    // Units of 256 rows keep the tensor cores busy with one half while the softmax of the other runs; of 128 there are more. Parts
-    // of the keys make more units still, for the price of writing and merging them. Estimated in us: a tile of keys takes 1.4
-    // (256 rows) or 1.1 (128), a unit 3 more, a merge 3 and its partials 1 per 4 MB; the call as long as its longest unit, or all of
-    // them over the SMs.
-    const int64_t most_q = d->max_q_len < d->num_q ? d->max_q_len : d->num_q;
-    const double mean = d->causal && most_k > 0 ? (double)tiles * (1.0 - 0.5 * (most_q < most_k ? most_q : most_k) / most_k) : (double)tiles;
-    double best = 1e300;
-    for (int half = 0; half < 2; ++half) {
-      const int64_t per = half ? kPromptTile : 2 * kPromptTile, units = entries_of(*d, per) * d->num_heads;
-      const int64_t most = d->num_splits > 0 ? d->num_splits : tiles < 64 ? (tiles > 1 ? tiles : 1) : 64;
-      for (int64_t s = d->num_splits > 0 ? d->num_splits : 1; s <= most; ++s) {
-        const double tile_us = half || most_q <= kPromptTile ? 1.1 : 1.4;
-        const double longest = 3 + tile_us * cdiv(tiles, s), all = units * s * (3 + tile_us * (mean / s < 1 ? 1 : mean / s)) / num_sms;
-        const double merge = s > 1 ? 3 + (double)rows * s * kHeadV * 4 / 4e6 : 0;
-        const double us = (longest > all ? longest : all) + merge;
-        if (us < best - 1e-9) {
-          best = us;
-          p.rows_per_unit = (int32_t)per;
-          p.num_splits = (int32_t)s;
-          p.units = units * s;
-        }
-      }
-    }
+    p.rows_per_unit = longest_q(*d) * p.pack <= kPromptTile ? kPromptTile : kMaxUnitRows;
     p.listed = d->num_seqs > 1;
+    const int64_t units = entries_of(*d, p.rows_per_unit) * (d->num_heads / p.pack);
+    p.shared = units > 0 && (d->num_ctas > 0 || (units < kSharedUnits * num_sms && tiles > kLeastShare));
+    p.ctas = !p.shared ? units : d->num_ctas > 0 ? d->num_ctas : num_sms;
+    if (p.shared && p.ctas > kMaxPromptCtas) p.ctas = kMaxPromptCtas;
+    if (p.shared)
+      p.workspace_bytes = pad(p.ctas * 2 * p.rows_per_unit * kHeadV * 4) + pad(p.ctas * 2 * p.rows_per_unit * 4) +
+                          pad(p.ctas * (int64_t)sizeof(PromptMerge)) + (p.listed ? pad((p.ctas + 2) * (int64_t)sizeof(PromptStart)) : 0);
+    if (p.listed) p.workspace_bytes += pad(entries_of(*d, p.rows_per_unit) * (int64_t)sizeof(int2));
   }
-  if (p.units > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
-  if (p.num_splits > 1) p.workspace_bytes = cdiv(rows * p.num_splits * kHeadV * 4, 256) * 256 + cdiv(rows * p.num_splits * 4, 256) * 256;
-  if (p.listed) p.workspace_bytes += cdiv(entries_of(*d, p.rows_per_unit) * (int64_t)sizeof(int2), 256) * 256;
+  if (p.ctas > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
   *plan = p;
   return MLA_OK;
 }
@@ -127,7 +118,6 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
 
   PromptArgs a;
   memset(&a, 0, sizeof a);
-  const int64_t rows = d->num_q * d->num_heads;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k_nope);
   a.kr = static_cast<const __nv_bfloat16*>(k_rope);
@@ -137,11 +127,16 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
   a.out = out;
   a.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  if (p.num_splits > 1) {
-    a.part_o = reinterpret_cast<float*>(ws);
-    ws += cdiv(rows * p.num_splits * kHeadV * 4, 256) * 256;
-    a.part_lse = reinterpret_cast<float*>(ws);
-    ws += cdiv(rows * p.num_splits * 4, 256) * 256;
+  const auto take = [&](int64_t bytes) {
+    char* at = ws;
+    ws += pad(bytes);
+    return at;
+  };
+  if (p.shared) {
+    a.part_o = reinterpret_cast<float*>(take(p.ctas * 2 * p.rows_per_unit * kHeadV * 4));
+    a.part_lse = reinterpret_cast<float*>(take(p.ctas * 2 * p.rows_per_unit * 4));
+    a.merges = reinterpret_cast<PromptMerge*>(take(p.ctas * (int64_t)sizeof(PromptMerge)));
+    if (p.listed) a.starts = reinterpret_cast<PromptStart*>(take((p.ctas + 2) * (int64_t)sizeof(PromptStart)));
   }
   a.list = reinterpret_cast<int2*>(ws);
   a.dev_status = dev_status;
@@ -160,13 +155,17 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
   a.max_q = d->max_q_len;
   a.max_k = d->max_k_len;
   a.causal = d->causal;
-  a.splits = p.num_splits;
+  a.pack = p.pack;
+  while ((1 << a.pack_log) < a.pack) ++a.pack_log;
+  a.virtual_heads = a.H / a.pack;
+  a.shared = p.shared;
+  a.ctas = (int32_t)p.ctas;
   a.rows_per_unit = p.rows_per_unit;
   a.entries = p.kernel == 0 ? entries_of(*d, p.rows_per_unit) : 0;
   a.listed = p.listed;
   const int64_t in_l2 = kGroupBytes / ((d->num_k > 0 ? d->num_k : 1) * 2 * (kNope + kHeadV));
-  const int64_t heads = (in_l2 > 1 ? in_l2 : 1) * a.group;
-  a.head_group = (int32_t)(heads < a.H ? heads : a.H);
+  const int64_t heads = (in_l2 > 1 ? in_l2 : 1) * (a.group / a.pack);  // virtual heads
+  a.head_group = (int32_t)(heads < a.virtual_heads ? heads : a.virtual_heads);
   a.out_f32 = d->out_dtype == MLA_DTYPE_F32;
   a.debug = debug ? 1 : 0;
   a.scale = d->softmax_scale;
@@ -174,9 +173,9 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
-  if (p.units > 0) {
+  if (p.ctas > 0) {
     if ((p.kernel == 1 ? launch_prompt_simt(a, s) : launch_prompt_tc(a, s)) != cudaSuccess) return MLA_ERR_CUDA;
-    if (p.num_splits > 1 && launch_prompt_merge(a, s) != cudaSuccess) return MLA_ERR_CUDA;
+    if (p.shared && launch_prompt_merge(a, s) != cudaSuccess) return MLA_ERR_CUDA;
   }
   if (!debug) return MLA_OK;
   mla_verify_desc checks = {};

@@ -10,7 +10,23 @@ constexpr int kNope = 128;                  // a head's own dims of a key
 constexpr int kHeadQ = kNope + kDRope;      // 192 dims of a query head
 constexpr int kHeadV = 128;                 // dims of a value
 constexpr int kPromptTile = 128;            // keys to a tile, and query rows to an MMA
-constexpr int kMaxPromptSplits = 1024;
+constexpr int kMaxPromptCtas = 1024;
+constexpr int kMaxUnitRows = 2 * kPromptTile;
+// What starting and ending a run of tiles costs, in tiles, and the least that a CTA takes in shared calls.
+constexpr int kUnitCost = 2, kLeastShare = 4;
+
+// Where a CTA of a shared call begins: its first entry, virtual head and tile there, or entry -1.
+struct PromptStart {
+  int32_t entry, head;
+  int64_t offset;
+};
+// A unit whose last part CTA number c computed, with the first one's CTA: parts first .. c, to be merged.
+struct PromptMerge {
+  int32_t live, first, slot;  // slot of the first part (the others have slot 0)
+  int32_t row0, rows;         // the unit's rows in its sequence, and how many there are
+  int32_t q0, head;
+  int32_t reserved;
+};
 
 struct PromptArgs {
   const __nv_bfloat16* q;
@@ -21,15 +37,18 @@ struct PromptArgs {
   const int32_t* cu_k;
   void* out;
   float* lse;
-  float* part_o;      // splits > 1: [splits][num_q * H][128], each part normalised over its own keys
-  float* part_lse;    // [splits][num_q * H]
-  int2* list;         // listed: (sequence, row tile) of every entry, longest first, then (-1, 0)
+  float* part_o;      // shared: [ctas][2][rows_per_unit][128], parts of units, each normalised over its own keys
+  float* part_lse;    // [ctas][2][rows_per_unit]
+  PromptMerge* merges;  // [ctas]
+  PromptStart* starts;  // shared and listed: [ctas]
+  int2* list;         // listed: (sequence, row tile) of every entry, longest first (shared: in order), then (-1, 0)
   int32_t* dev_status;
   int64_t num_q, num_k;
   int64_t q_ts, q_hs, k_ts, k_hs, kr_ts, v_ts, v_hs;
   int64_t entries;    // row tiles of all sequences, at most
   int32_t B, H, group, max_q, max_k;
-  int32_t causal, splits, rows_per_unit, listed, head_group, out_f32, debug;
+  int32_t pack, pack_log, virtual_heads;  // rows of a unit: pack heads a query; H / pack of such groups
+  int32_t causal, shared, ctas, rows_per_unit, listed, head_group, out_f32, debug;
   float scale, scale_log2;
 };
 
@@ -71,11 +90,11 @@ __device__ __forceinline__ int sequence_of(const PromptArgs& a, int64_t row, Pro
   s = load_seq(a, lo);
   return row >= s.q0 && row < (int64_t)s.q0 + s.m ? lo : -1;
 }
-// The tiles [t0, t1) of part `split` when `tiles` tiles are cut into a.splits parts of one size.
-__device__ __forceinline__ void part_of(const PromptArgs& a, int32_t tiles, int32_t split, int32_t& t0, int32_t& t1) {
-  const int32_t each = (tiles + a.splits - 1) / a.splits;
-  t0 = (int32_t)min((int64_t)tiles, (int64_t)each * split);
-  t1 = min(tiles, t0 + each);
+// Tiles of keys that a unit's rows [row0, row1) of a sequence see.
+__device__ __forceinline__ int32_t tiles_of(const PromptArgs& a, const PromptSeq& s, int64_t row1) {
+  return (int32_t)(((int64_t)visible(a, s, (int32_t)((row1 - 1) >> a.pack_log)) + kPromptTile - 1) / kPromptTile);
 }
+// Units of work of an entry and virtual head: its tiles, at least one, and what a run costs besides.
+__device__ __forceinline__ int64_t cost_of(int32_t tiles) { return max(1, tiles) + kUnitCost; }
 
 }  // namespace mla

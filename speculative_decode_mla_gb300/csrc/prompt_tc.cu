@@ -1,24 +1,28 @@
 // tcgen05 prompt attention for sm_103a (include/mla_prompt.h).
 //
-// A unit is up to 256 query rows (two lanes of 128) of one head and a part of the keys that they see. A CTA works
-// through units; the next one's number comes from cancelling a CTA that has not started (clusterlaunchcontrol),
-// so units go, in index order (heads in groups whose keys and values stay in L2; inside a group longest first),
-// to whichever SM is free, with no counter in memory. Per tile of 128 keys and lane:
+// A unit is up to 256 rows (two lanes of 128) of one sequence; a row is a query and a head, and the heads that share a key
+// head lie side by side (pack). A CTA works through units, or, in calls with few of them, through an equal share of all units'
+// tiles of 128 keys (a share may begin and end inside a unit; prompt_merge_kernel joins such parts). In calls of many units the
+// next one's number comes from cancelling a CTA that has not started (clusterlaunchcontrol), so units go, in index
+// order (heads in groups whose keys and values stay in L2; inside a group longest first), to whichever SM is free, with no
+// counter in memory. Per tile and lane:
 //
 //   S = Q K^T   M = 128, N = 128, 12 K-steps: 8 over the head's own dims, 4 over the shared RoPE dims
 //   P = 2^((S - m) scale log2 e) as bf16, in S's place in TMEM; the running maximum is kept in the sums' own units and
 //       taken away before the scale, so that large scores lose nothing; O is rescaled only when it grows by more than 2^8
 //   O += P V    M = 128, N = 128, 8 K-steps, P from TMEM
 //
-// While one lane's softmax runs, the tensor cores work for the other lane.
+// While one lane's softmax runs, the tensor cores work for the other lane. When no sequence has more than 128 rows (ONE), there
+// is one lane with two S buffers: S of the next tile is ready when the softmax has done with this one, and the other lane's
+// shared memory makes the ring longer, since such calls wait for keys and values.
 //
-//   warps 0-3, 4-7  softmax of lane 0, 1: a thread a row; they also write O / l out
-//   warp 8          TMA loads, and the units
-//   warp 9          MMA issue, one thread
+//   warps 0-3 (, 4-7)  softmax of lane 0 (, 1): a thread a row; they also write O / l out
+//   next warp          TMA loads, and the units
+//   last warp          MMA issue, one thread
 //
-// TMEM (512 columns): S of lane 0, 1 [0, 256), O of lane 0, 1 [256, 512). Shared memory: Q 96 KB, and a ring of eight
-// 16 KB blocks which a tile's keys (three blocks of 64 dims) and values (two blocks of 64 keys) go through in the order
-// of their use, K(0) V(0) K(1) V(1) ..., each block free for the next load as soon as both lanes' MMAs are done with it.
+// TMEM (512 columns): two S [0, 256), two O [256, 512). Shared memory: Q, 48 KB a lane, and a ring of 16 KB blocks (8, with ONE
+// 11) which a tile's keys (three blocks of 64 dims) and values (two blocks of 64 keys) go through in the order
+// K(0) V(0) K(1) V(1) ..., each block free for the next load as soon as all MMAs are done with it.
 //
 // A key that a row does not see has a score of -inf there. Values in tiles that some row of the unit does not see whole
 // (on the diagonal, behind the sequence's end) are looked through first: rows behind the end become 0, and
@@ -35,26 +39,25 @@ namespace {
 constexpr int kRows = kPromptTile, kKeys = kPromptTile;
 constexpr int kBlock = 16384;                 // 128 rows x 64 dims (Q, K) or 64 keys x 128 dims (V), 128B swizzle
 constexpr int kQBytes = 3 * kBlock;           // a lane's queries
-constexpr int kSlots = 8;
 constexpr int kTileBlocks = 5;
-constexpr int kSmemQ = 0;
-constexpr int kSmemRing = 2 * kQBytes;
-constexpr int kSmemBar = kSmemRing + kSlots * kBlock;
-constexpr int kThreads = 320;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
-
-constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarQFull = 2 * kSlots /*2*/, kBarQEmpty = kBarQFull + 2 /*2*/,
-              kBarS = kBarQEmpty + 2 /*2*/, kBarP = kBarS + 2 /*2*/, kBarO = kBarP + 2 /*2*/, kBarUnit = kBarO + 2 /*2*/,
-              kBarUnitEmpty = kBarUnit + 2 /*2*/, kBarNext = kBarUnitEmpty + 2, kBarDrain = kBarNext + 1, kNumBars = kBarDrain + 1;
-constexpr int kSmemNext = kSmemBar + 512;     // 16 bytes: the answer to a cancel request
-constexpr int kSmemUnit = kSmemNext + 16;     // two unit descriptions
+constexpr int kMaxSpecial = 3;                // tiles that some row of a unit does not see whole, and another does in part
 constexpr int kUnitWords = 24;
-constexpr int kSmemBad = kSmemUnit + 2 * kUnitWords * 4;  // [2][kMaxSpecial][4] words: keys whose values are not all finite
-constexpr int kMaxSpecial = 3;
-constexpr int kSmemFlags = kSmemBad + 2 * kMaxSpecial * 16;  // TMEM address, abort flag
-constexpr int kSmemBytes = kSmemFlags + 16 + 1024;
-static_assert(8 * kNumBars <= 512 && kSmemBytes <= 232448, "shared memory");
+
+template <bool ONE>
+struct Layout {
+  static constexpr int lanes = ONE ? 1 : 2, slots = ONE ? 11 : 8;
+  static constexpr int load_warp = 4 * lanes, mma_warp = load_warp + 1, threads = 32 * (mma_warp + 1);
+  static constexpr int ring = lanes * kQBytes, bars = ring + slots * kBlock;
+  static constexpr int full = 0, empty = slots, q_full = 2 * slots /*2*/, q_empty = q_full + 2 /*2*/, s = q_empty + 2 /*2*/, p = s + 2 /*2*/,
+                       o = p + 2 /*2*/, unit = o + 2 /*2*/, unit_empty = unit + 2 /*2*/, next = unit_empty + 2, drain = next + 1, num_bars = drain + 1;
+  static constexpr int answer = bars + 512;                // 16 bytes: the answer to a cancel request
+  static constexpr int units = answer + 16;                // two unit descriptions
+  static constexpr int bad = units + 2 * kUnitWords * 4;   // [2][kMaxSpecial][4] words: keys whose values are not all finite
+  static constexpr int flags = bad + 2 * kMaxSpecial * 16; // TMEM address, abort flag
+  static constexpr int bytes = flags + 16 + 1024;
+  static_assert(8 * num_bars <= 512 && bytes <= 232448 && answer % 16 == 0, "shared memory");
+};
 
 #define TMEM_LD32(addr, r)                                                                                              \
   asm volatile(                                                                                                         \
@@ -127,90 +130,196 @@ __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
   }
 }
 
-// What every role needs to know of a unit. Lane r's rows are [row0 + 128 r, row0 + 128 r + 128) of the sequence, of which
-// those below m exist; it works on the tiles [t0, t0 + tiles[r]). `special`: the first tile that some row does not see whole.
+// What every role needs to know of a unit, or of a part of one. Lane r's rows are [row0 + 128 r, row0 + 128 r + 128) of the
+// sequence, of which those below `rows` exist; it works on the tiles [t0, t0 + tiles[r]). `special`: the first tile that some row does
+// not see whole. `part`: where its result goes in part_o, -1: to out.
 struct Unit {
   int32_t live;      // 0: there is no further unit
-  int32_t row0, h, g, split;
+  int32_t row0, rows, h, g, part;
   PromptSeq s;
+  int32_t all;       // tiles of the whole unit
   int32_t t0, special;
   int32_t tiles[2];
 };
 static_assert(sizeof(Unit) <= kUnitWords * 4, "unit description");
 
-// Unit number u (heads in groups of a.head_group; in a group by row tile, then part, then head).
-__device__ __forceinline__ Unit unit_at(const PromptArgs& a, int64_t u) {
+// Row tile `tile` of sequence b (-1: none), heads of virtual head vh, all tiles.
+__device__ __forceinline__ Unit unit_of(const PromptArgs& a, int b, int tile, int vh) {
   Unit x;
-  const int64_t full = a.entries * a.splits * a.head_group, group = u / full;
-  const int heads = min(a.head_group, a.H - (int)group * a.head_group);
-  const int64_t rest = u - group * full, per = (int64_t)a.splits * heads, e = rest / per;
-  const int in = (int)(rest - e * per);
-  x.split = in / heads;
-  x.h = (int)group * a.head_group + in % heads;
-  x.g = x.h / a.group;
   x.live = 1;
-  x.t0 = x.special = x.tiles[0] = x.tiles[1] = x.row0 = 0;
+  x.part = -1;
+  x.h = vh * a.pack;
+  x.g = x.h / a.group;
+  x.t0 = x.special = x.tiles[0] = x.tiles[1] = x.row0 = x.rows = x.all = 0;
+  x.s.q0 = x.s.m = x.s.k0 = x.s.n = 0;
+  if (b < 0) return x;
+  x.s = load_seq(a, b);
+  const int64_t rows = (int64_t)x.s.m << a.pack_log, row0 = (int64_t)tile * a.rows_per_unit;
+  if (row0 >= rows) return x;
+  x.row0 = (int32_t)row0;
+  x.rows = (int32_t)rows;
+  x.all = tiles_of(a, x.s, min(rows, row0 + a.rows_per_unit));
+  x.special = visible(a, x.s, x.row0 >> a.pack_log) / kKeys;
+  return x;
+}
+// Its tiles [t0, t1).
+__device__ __forceinline__ void cut(const PromptArgs& a, Unit& x, int32_t t0, int32_t t1) {
+  const int64_t mid = (int64_t)x.row0 + kRows;
+  x.t0 = t0;
+  x.tiles[0] = x.all ? max(0, min(t1, tiles_of(a, x.s, min((int64_t)x.rows, mid))) - t0) : 0;
+  x.tiles[1] = a.rows_per_unit > kRows && x.rows > mid ? t1 - t0 : 0;
+}
+// Unit number u of a call that is not shared (virtual heads in groups of a.head_group; in a group by row tile, then head).
+__device__ __forceinline__ Unit unit_at(const PromptArgs& a, int64_t u) {
+  const int64_t full = a.entries * a.head_group, group = u / full;
+  const int heads = min(a.head_group, a.virtual_heads - (int)group * a.head_group);
+  const int64_t rest = u - group * full, e = rest / heads;
+  const int vh = (int)group * a.head_group + (int)(rest - e * heads);
   int b = 0, tile = (int)(a.entries - 1 - e);
   if (a.listed) {
     const int2 at = a.list[e];
     b = at.x;
     tile = at.y;
   }
-  if (b < 0) {
-    x.s.q0 = x.s.m = x.s.k0 = x.s.n = 0;
-    return x;
-  }
-  x.s = load_seq(a, b);
-  x.row0 = tile * a.rows_per_unit;
-  if (x.row0 >= x.s.m) {
-    x.s.m = 0;
-    return x;
-  }
-  const int last = min(x.s.m, x.row0 + a.rows_per_unit) - 1;
-  const auto tiles_of = [&](int row) { return (int)(((int64_t)visible(a, x.s, row) + kKeys - 1) / kKeys); };
-  int32_t t1;
-  part_of(a, tiles_of(last), x.split, x.t0, t1);
-  x.tiles[0] = max(0, min(t1, tiles_of(min(last, x.row0 + kRows - 1))) - x.t0);
-  x.tiles[1] = last - x.row0 >= kRows ? max(0, t1 - x.t0) : 0;
-  x.special = visible(a, x.s, x.row0) / kKeys;
+  Unit x = unit_of(a, b, tile, vh);
+  cut(a, x, 0, x.all);
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// A CTA's way through its share of a shared call: entries in order, the virtual heads of an entry one after the other, each
+// cost_of(its tiles) units of work, of which the last kUnitCost stand for starting and ending it.
+struct Walk {
+  int64_t w, w_end, offset, share;  // offset: of w in the unit
+  int32_t entry, head;
+  bool first;
+};
+// Where share number c begins (every lane of the warp calls it).
+__device__ __forceinline__ Walk walk_from(const PromptArgs& a, int c, int lane) {
+  Walk k;
+  k.first = true;
+  if (a.listed) {
+    const PromptStart s = a.starts[c];
+    k.entry = s.entry;
+    k.head = s.head;
+    k.offset = s.offset;
+    k.share = a.starts[a.ctas].offset;
+    k.w = (int64_t)c * k.share;
+    k.w_end = s.entry < 0 ? k.w : min(k.w + k.share, a.starts[a.ctas + 1].offset);
+    return k;
+  }
+  const PromptSeq s = load_seq(a, 0);
+  const int64_t rows = (int64_t)s.m << a.pack_log;
+  const int64_t n = (rows + a.rows_per_unit - 1) / a.rows_per_unit;
+  const auto cost = [&](int64_t e) { return e < n ? cost_of(tiles_of(a, s, min(rows, (e + 1) * a.rows_per_unit))) : 0; };
+  int64_t total = 0;
+  for (int64_t e = lane; e < n; e += 32) total += cost(e);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  total *= a.virtual_heads;
+  k.share = max((int64_t)kLeastShare + kUnitCost, (total + a.ctas - 1) / a.ctas);
+  k.w = min(total, c * k.share);
+  k.w_end = min(total, k.w + k.share);
+  k.entry = -1;
+  int64_t before = 0;
+  for (int64_t e0 = 0; e0 < n && k.w < k.w_end; e0 += 32) {
+    const int64_t own = cost(e0 + lane) * a.virtual_heads;
+    int64_t inc = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > k.w);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int64_t in = k.w - before - __shfl_sync(0xffffffffu, inc - own, l), per = __shfl_sync(0xffffffffu, own, l) / a.virtual_heads;
+      k.entry = (int32_t)e0 + l;
+      k.head = (int32_t)(in / per);
+      k.offset = in - k.head * per;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return k;
+}
+// The next part of the share; not live when it is done. The unit that ends with a part of this share, but began before it, is
+// the first one, if any: *merge says so.
+__device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, PromptMerge* merge) {
+  Unit x;
+  x.live = 0;
+  while (k.w < k.w_end) {
+    int b = 0, tile = k.entry;
+    if (a.listed) {
+      const int2 at = a.list[k.entry];
+      b = at.x;
+      tile = at.y;
+    }
+    x = unit_of(a, b, tile, k.head);
+    const int64_t len = max(1, x.all), off = k.offset, take = min(len - off, k.w_end - k.w);
+    if (off < len) {
+      cut(a, x, (int32_t)off, (int32_t)min((int64_t)x.all, off + take));
+      if (off > 0 || take < len) x.part = 2 * c + (k.first ? 0 : 1);
+      if (off > 0 && off + take == len) {
+        const int64_t begin = k.w - off;
+        merge->first = (int32_t)(begin / k.share);
+        merge->slot = begin % k.share ? 1 : 0;
+        merge->row0 = x.row0;
+        merge->rows = min(a.rows_per_unit, x.rows - x.row0);
+        merge->q0 = x.s.q0;
+        merge->head = x.h;
+        merge->live = 1;
+      }
+    }
+    k.first = false;
+    // on to the next unit
+    k.w += len + kUnitCost - off;
+    k.offset = 0;
+    if (++k.head == a.virtual_heads) {
+      k.head = 0;
+      ++k.entry;
+    }
+    if (off < len) return x;
+    x.live = 0;
+  }
+  return x;
+}
+
+template <bool ONE>
+__global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_kr, const __grid_constant__ CUtensorMap map_v) {
+  using L = Layout<ONE>;
+  constexpr uint32_t kSlots = L::slots;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw), base = (raw_addr + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw_addr);
-  const auto bar = [&](int i) { return base + kSmemBar + 8u * (uint32_t)i; };
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + kSmemFlags);
+  const auto bar = [&](int i) { return base + L::bars + 8u * (uint32_t)i; };
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::flags);
   volatile uint32_t* const abort_flag = tmem_slot + 1;
-  Unit* const units = reinterpret_cast<Unit*>(smem + kSmemUnit);
-  const auto unit_slot = [&](int i) { return reinterpret_cast<Unit*>(smem + kSmemUnit + i * kUnitWords * 4); };
-  (void)units;
-  uint32_t* const bad = reinterpret_cast<uint32_t*>(smem + kSmemBad);
+  const auto unit_slot = [&](int i) { return reinterpret_cast<Unit*>(smem + L::units + i * kUnitWords * 4); };
+  uint32_t* const bad = reinterpret_cast<uint32_t*>(smem + L::bad);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(bar(kBarFull + i), 1);
-      mbar_init(bar(kBarEmpty + i), 1);
+    for (int i = 0; i < L::slots; ++i) {
+      mbar_init(bar(L::full + i), 1);
+      mbar_init(bar(L::empty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarQFull + i), 1);
-      mbar_init(bar(kBarQEmpty + i), 1);
-      mbar_init(bar(kBarS + i), 1);
-      mbar_init(bar(kBarP + i), 4);
-      mbar_init(bar(kBarO + i), 1);
-      mbar_init(bar(kBarUnit + i), 1);
-      mbar_init(bar(kBarUnitEmpty + i), 9);
+      mbar_init(bar(L::q_full + i), 1);
+      mbar_init(bar(L::q_empty + i), 1);
+      mbar_init(bar(L::s + i), 1);
+      mbar_init(bar(L::p + i), 4);
+      mbar_init(bar(L::o + i), 1);
+      mbar_init(bar(L::unit + i), 1);
+      mbar_init(bar(L::unit_empty + i), 1 + 4 * L::lanes);
     }
-    mbar_init(bar(kBarNext), 1);
-    mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(L::next), 1);
+    mbar_init(bar(L::drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == L::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -222,14 +331,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // everything above read no global memory
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == kLoadWarp) {
+  if (warp == L::load_warp) {
     // ------------------------------------------------------------------------------ loads and units
+    Walk walk = {};
+    if (a.shared) walk = walk_from(a, blockIdx.x, lane);
     if (elect_one()) {
       uint32_t blocks = 0, q_loads[2] = {0, 0};  // ring blocks and query tiles loaded so far
       const auto load_block = [&](const CUtensorMap* map, int x, int y, int z, bool value) {
         const uint32_t slot = blocks % kSlots, use = blocks / kSlots;
-        if (use > 0 && !wait_bar(bar(kBarEmpty + slot), (use - 1) & 1, abort_flag)) return false;
-        const uint32_t dst = base + kSmemRing + slot * kBlock, full = bar(kBarFull + slot);
+        if (use > 0 && !wait_bar(bar(L::empty + slot), (use - 1) & 1, abort_flag)) return false;
+        const uint32_t dst = base + L::ring + slot * kBlock, full = bar(L::full + slot);
         mbar_arrive_expect_tx(full, kBlock);
         tma_load3(dst, map, x, y, z, full);
         if (value) tma_load3(dst + kBlock / 2, map, x + 64, y, z, full);
@@ -240,155 +351,185 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n_unit = 0;
       int64_t u = blockIdx.x;
       bool ok = true;
+      PromptMerge merge = {};
       while (ok) {
         const int slot = n_unit & 1;
-        if (n_unit >= 2 && !wait_bar(bar(kBarUnitEmpty + slot), ((n_unit >> 1) - 1) & 1, abort_flag)) break;
+        if (n_unit >= 2 && !wait_bar(bar(L::unit_empty + slot), ((n_unit >> 1) - 1) & 1, abort_flag)) break;
         Unit x;
-        if (u >= 0) x = unit_at(a, u);
-        else x.live = 0;
+        x.live = 0;
+        if (a.shared) {
+          x = next_part(a, walk, blockIdx.x, &merge);
+          if (n_unit == 0) a.merges[blockIdx.x] = merge;
+        } else if (u >= 0) {
+          x = unit_at(a, u);
+        }
         *unit_slot(slot) = x;
-        mbar_arrive(bar(kBarUnit + slot));
+        mbar_arrive(bar(L::unit + slot));
         if (!x.live) break;
-        // ask for the unit after this one
-        mbar_arrive_expect_tx(bar(kBarNext), 16);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                         base + kSmemNext),
-                     "r"(bar(kBarNext))
-                     : "memory");
-        next_asked = true;
+        if (!a.shared) {  // ask for the unit after this one
+          mbar_arrive_expect_tx(bar(L::next), 16);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                           base + L::answer),
+                       "r"(bar(L::next))
+                       : "memory");
+          next_asked = true;
+        }
         const int n = max(x.tiles[0], x.tiles[1]);
         const auto load_q = [&](int r) {
           if (x.tiles[r] == 0) return true;
-          if (q_loads[r] > 0 && !wait_bar(bar(kBarQEmpty + r), (q_loads[r] - 1) & 1, abort_flag)) return false;
-          const uint32_t full = bar(kBarQFull + r);
+          if (q_loads[r] > 0 && !wait_bar(bar(L::q_empty + r), (q_loads[r] - 1) & 1, abort_flag)) return false;
+          const uint32_t full = bar(L::q_full + r);
           mbar_arrive_expect_tx(full, kQBytes);
           for (int i = 0; i < 3; ++i)
-            tma_load3(base + kSmemQ + r * kQBytes + i * kBlock, &map_q, 64 * i, x.h, x.s.q0 + x.row0 + r * kRows, full);
+            tma_load3(base + r * kQBytes + i * kBlock, &map_q, 64 * i, x.h, x.s.q0 + ((x.row0 + r * kRows) >> a.pack_log), full);
           ++q_loads[r];
           return true;
         };
         for (int j = 0; j < n && ok; ++j) {
           const int at = x.s.k0 + (x.t0 + j) * kKeys;
           ok = load_block(&map_k, 0, x.g, at, false) && load_block(&map_k, 64, x.g, at, false) && load_block(&map_kr, 0, 0, at, false);
-          if (ok && j == 0) ok = load_q(0) && load_q(1);
+          if (ok && j == 0) ok = load_q(0) && (ONE || load_q(1));
           ok = ok && load_block(&map_v, 0, x.g, at, true) && load_block(&map_v, 0, x.g, at + 64, true);
         }
-        if (!ok || !wait_bar(bar(kBarNext), n_unit & 1, abort_flag)) break;
-        next_asked = false;
-        uint32_t got, id;
-        asm volatile(
-            "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b64 lo, hi;\n"
-            "ld.shared.v2.b64 {lo, hi}, [%2];\nmov.b128 h, {lo, hi};\n"
-            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
-            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
-            : "=r"(got), "=r"(id)
-            : "r"(base + kSmemNext)
-            : "memory");
-        u = got ? (int64_t)id : -1;
+        if (ok && !a.shared) {
+          ok = wait_bar(bar(L::next), n_unit & 1, abort_flag);
+          if (!ok) break;
+          next_asked = false;
+          uint32_t got, id;
+          asm volatile(
+              "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b64 lo, hi;\n"
+              "ld.shared.v2.b64 {lo, hi}, [%2];\nmov.b128 h, {lo, hi};\n"
+              "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+              "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
+              : "=r"(got), "=r"(id)
+              : "r"(base + L::answer)
+              : "memory");
+          u = got ? (int64_t)id : -1;
+        }
         ++n_unit;
       }
       if (*abort_flag) {  // what is in flight lands before the CTA ends
-        if (next_asked) drain_bar(bar(kBarNext), n_unit & 1);
-        for (uint32_t i = blocks > kSlots ? blocks - kSlots : 0; i < blocks; ++i) drain_bar(bar(kBarFull + i % kSlots), (i / kSlots) & 1);
+        if (next_asked) drain_bar(bar(L::next), n_unit & 1);
+        for (uint32_t i = blocks > kSlots ? blocks - kSlots : 0; i < blocks; ++i) drain_bar(bar(L::full + i % kSlots), (i / kSlots) & 1);
         for (int r = 0; r < 2; ++r)
-          if (q_loads[r]) drain_bar(bar(kBarQFull + r), (q_loads[r] - 1) & 1);
+          if (q_loads[r]) drain_bar(bar(L::q_full + r), (q_loads[r] - 1) & 1);
         report(a.dev_status, a.dev_status != nullptr, MLA_CHECK_TIMEOUT);
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == L::mma_warp) {
     // ------------------------------------------------------------------------------ MMA issue
     if (elect_one()) {
       constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_pv = instr_desc(kHeadV, 1);
-      uint32_t blocks = 0, p_uses[2] = {0, 0}, q_uses[2] = {0, 0};
+      uint32_t blocks = 0, p_uses[2] = {0, 0}, q_uses[2] = {0, 0}, tiles = 0;  // (tiles: of ONE, in all units)
       bool issued = false;
-      const auto landed = [&](uint32_t i) { return wait_bar(bar(kBarFull + i % kSlots), (i / kSlots) & 1, abort_flag); };
-      const auto block_at = [&](uint32_t i) { return base + kSmemRing + (i % kSlots) * kBlock; };
-      // S of lane r over the tile whose first block is `first`
-      const auto scores = [&](int r, uint32_t first, bool last) {
+      const auto landed = [&](uint32_t i) { return wait_bar(bar(L::full + i % kSlots), (i / kSlots) & 1, abort_flag); };
+      const auto block_at = [&](uint32_t i) { return base + L::ring + (i % kSlots) * kBlock; };
+      // S buffer s = Q of lane r times the keys of the tile whose first block is `first`
+      const auto scores = [&](int r, int s, uint32_t first, bool last) {
         for (int i = 0; i < 3; ++i) {
           if (!landed(first + i)) return false;
-          const uint32_t qa = base + kSmemQ + r * kQBytes + i * kBlock, kb = block_at(first + i);
+          const uint32_t qa = base + r * kQBytes + i * kBlock, kb = block_at(first + i);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_smem_a(tmem + kColS + 128 * r, smem_desc(qa + kk * 32, 16, 1024), smem_desc(kb + kk * 32, 16, 1024), idesc_s,
+            mma_smem_a(tmem + kColS + 128 * s, smem_desc(qa + kk * 32, 16, 1024), smem_desc(kb + kk * 32, 16, 1024), idesc_s,
                        i > 0 || kk > 0);
         }
         issued = true;
-        mma_commit(bar(kBarS + r));
-        if (last) mma_commit(bar(kBarQEmpty + r));
+        mma_commit(bar(L::s + s));
+        if (last) mma_commit(bar(L::q_empty + r));
         return true;
       };
-      // O of lane r += P V
-      const auto values = [&](int r, uint32_t first, bool begins) {
-        if (!wait_bar(bar(kBarP + r), p_uses[r] & 1, abort_flag)) return false;
-        ++p_uses[r];
+      // O of lane r += P (in S buffer s) V
+      const auto values = [&](int r, int s, uint32_t first, bool begins) {
+        if (!wait_bar(bar(L::p + s), p_uses[s] & 1, abort_flag)) return false;
+        ++p_uses[s];
         tc_fence_after();
         for (int i = 0; i < 2; ++i) {
           if (!landed(first + 3 + i)) return false;
           const uint32_t vb = block_at(first + 3 + i);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_tmem_a(tmem + kColO + 128 * r, tmem + kColS + 128 * r + (i * 4 + kk) * 8, smem_desc(vb + kk * 2048, kBlock / 2, 1024),
+            mma_tmem_a(tmem + kColO + 128 * r, tmem + kColS + 128 * s + (i * 4 + kk) * 8, smem_desc(vb + kk * 2048, kBlock / 2, 1024),
                        idesc_pv, !begins || i > 0 || kk > 0);
         }
         issued = true;
-        mma_commit(bar(kBarO + r));
+        mma_commit(bar(L::o + r));
         return true;
       };
       const auto free_blocks = [&](uint32_t first, int n) {
-        for (int i = 0; i < n; ++i) mma_commit(bar(kBarEmpty + (first + i) % kSlots));
+        for (int i = 0; i < n; ++i) mma_commit(bar(L::empty + (first + i) % kSlots));
       };
       for (uint32_t n_unit = 0;; ++n_unit) {
         const int slot = n_unit & 1;
-        if (!wait_bar(bar(kBarUnit + slot), (n_unit >> 1) & 1, abort_flag)) break;
+        if (!wait_bar(bar(L::unit + slot), (n_unit >> 1) & 1, abort_flag)) break;
         const Unit x = *unit_slot(slot);
-        mbar_arrive(bar(kBarUnitEmpty + slot));
+        mbar_arrive(bar(L::unit_empty + slot));
         if (!x.live) break;
         const int n0 = x.tiles[0], n1 = x.tiles[1], n = max(n0, n1);
         if (n == 0) continue;
         bool ok = true;
-        if (n0) ok = wait_bar(bar(kBarQFull + 0), q_uses[0]++ & 1, abort_flag) && scores(0, blocks, n0 == 1);
-        if (ok && n1) ok = wait_bar(bar(kBarQFull + 1), q_uses[1]++ & 1, abort_flag) && scores(1, blocks, n1 == 1);
-        if (ok) free_blocks(blocks, 3);
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t here = blocks + kTileBlocks * j, next = here + kTileBlocks;
-          if (j < n0) ok = values(0, here, j == 0);
-          if (ok && j + 1 < n0) ok = scores(0, next, j + 2 == n0);
-          if (ok && j < n1) ok = values(1, here, j == 0);
-          if (ok) free_blocks(here + 3, 2);
-          if (ok && j + 1 < n1) ok = scores(1, next, j + 2 == n1);
-          if (ok && j + 1 < n) free_blocks(next, 3);
+        if (ONE) {  // tiles take the S buffers in turn, across units too
+          ok = wait_bar(bar(L::q_full + 0), q_uses[0]++ & 1, abort_flag);
+          for (int j = 0; j < min(2, n) && ok; ++j) {
+            ok = scores(0, (tiles + j) & 1, blocks + kTileBlocks * j, j + 1 == n);
+            if (ok) free_blocks(blocks + kTileBlocks * j, 3);
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t here = blocks + kTileBlocks * j, next = here + 2 * kTileBlocks;
+            ok = values(0, (tiles + j) & 1, here, j == 0);
+            if (ok) free_blocks(here + 3, 2);
+            if (ok && j + 2 < n) {
+              ok = scores(0, (tiles + j) & 1, next, j + 3 == n);
+              if (ok) free_blocks(next, 3);
+            }
+          }
+          tiles += n;
+        } else {
+          if (n0) ok = wait_bar(bar(L::q_full + 0), q_uses[0]++ & 1, abort_flag) && scores(0, 0, blocks, n0 == 1);
+          if (ok && n1) ok = wait_bar(bar(L::q_full + 1), q_uses[1]++ & 1, abort_flag) && scores(1, 1, blocks, n1 == 1);
+          if (ok) free_blocks(blocks, 3);
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t here = blocks + kTileBlocks * j, next = here + kTileBlocks;
+            if (j < n0) ok = values(0, 0, here, j == 0);
+            if (ok && j + 1 < n0) ok = scores(0, 0, next, j + 2 == n0);
+            if (ok && j < n1) ok = values(1, 1, here, j == 0);
+            if (ok) free_blocks(here + 3, 2);
+            if (ok && j + 1 < n1) ok = scores(1, 1, next, j + 2 == n1);
+            if (ok && j + 1 < n) free_blocks(next, 3);
+          }
         }
         if (!ok) break;
         blocks += kTileBlocks * n;
       }
       if (*abort_flag && issued) {
-        mma_commit(bar(kBarDrain));
-        drain_bar(bar(kBarDrain), 0);
+        mma_commit(bar(L::drain));
+        drain_bar(bar(L::drain), 0);
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------------------ softmax and output
     const int r = warp >> 2, in_warp = (warp & 3) * 32, row = in_warp + lane;  // lane of the unit, row of the lane
-    const uint32_t tS = tmem + ((uint32_t)in_warp << 16) + kColS + 128 * r, tO = tmem + ((uint32_t)in_warp << 16) + kColO + 128 * r;
+    const uint32_t lanes = (uint32_t)in_warp << 16, tO = tmem + lanes + kColO + 128 * r;
     uint32_t blocks = 0, tile_uses = 0;  // ring blocks of the units before; tiles of this lane so far
     bool ok = true;
     for (uint32_t n_unit = 0; ok; ++n_unit) {
       const int slot = n_unit & 1;
-      if (!wait_warp(bar(kBarUnit + slot), (n_unit >> 1) & 1, abort_flag)) break;
+      if (!wait_warp(bar(L::unit + slot), (n_unit >> 1) & 1, abort_flag)) break;
       const Unit x = *unit_slot(slot);
       if (!x.live) break;
       const int n = x.tiles[r], unit_tiles = max(x.tiles[0], x.tiles[1]), other = x.tiles[r ^ 1];
-      const int i = x.row0 + r * kRows + row;  // this thread's query
-      const bool real = i < x.s.m && r * kRows < a.rows_per_unit;
-      const int32_t vis = real ? visible(a, x.s, i) : 0;
+      const int at = x.row0 + r * kRows + row;  // this thread's row
+      const bool real = at < x.rows;
+      const int32_t vis = real ? visible(a, x.s, at >> a.pack_log) : 0;
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
       for (int j = 0; j < n; ++j) {
-        if (!wait_warp(bar(kBarS + r), tile_uses & 1, abort_flag)) {
+        const int buf = ONE ? (int)(tile_uses & 1) : r;
+        const uint32_t tS = tmem + lanes + kColS + 128 * buf;
+        if (!wait_warp(bar(L::s + buf), (ONE ? tile_uses >> 1 : tile_uses) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -430,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l.x *= keep;
           l.y *= keep;
           if (j > 0) {
-            if (!wait_warp(bar(kBarO + r), (tile_uses - 1) & 1, abort_flag)) {
+            if (!wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -466,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tile >= x.special && (r == 0 || j >= other)) {
           // the first lane that uses the tile looks through its values: thread `row` has key `row`
           const uint32_t block = blocks + kTileBlocks * j + 3 + (row >> 6);
-          if (!wait_warp(bar(kBarFull + block % kSlots), (block / kSlots) & 1, abort_flag)) {
+          if (!wait_warp(bar(L::full + block % kSlots), (block / kSlots) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          uint4* const at = reinterpret_cast<uint4*>(smem + kSmemRing + (block % kSlots) * kBlock + (row & 63) * 128);
+          uint4* const at = reinterpret_cast<uint4*>(smem + L::ring + (block % kSlots) * kBlock + (row & 63) * 128);
           const bool behind = (int64_t)tile * kKeys + row >= x.s.n;
           bool odd = false;
 #pragma unroll
@@ -493,13 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + r));
+        if (lane == 0) mbar_arrive(bar(L::p + buf));
         ++tile_uses;
       }
       // the last product of this lane, then O / l
-      if (ok && n > 0 && !wait_warp(bar(kBarO + r), (tile_uses - 1) & 1, abort_flag)) ok = false;
-      const int64_t rh = (int64_t)(x.s.q0 + (int64_t)i) * a.H + x.h, rows = a.num_q * a.H;
-      float* const lse_at = a.splits > 1 ? a.part_lse + x.split * rows + rh : a.lse + rh;
+      if (ok && n > 0 && !wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) ok = false;
+      const int64_t rh = (int64_t)(x.s.q0 + (at >> a.pack_log)) * a.H + x.h + (at & (a.pack - 1));
+      const int64_t part = (int64_t)x.part * a.rows_per_unit + r * kRows + row;
+      float* const lse_at = x.part >= 0 ? a.part_lse + part : a.lse + rh;
       if (!ok) {
         if (real) *lse_at = NAN;
         break;
@@ -507,9 +649,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : 1.f / sum;
       if (real) *lse_at = sum == 0.f ? -INFINITY : m * a.scale + logf(sum);
-      uint32_t odd = 0;  // does the unit have values that are not finite?
-      const int specials = max(0, x.t0 + unit_tiles - max(x.t0, x.special));
-      for (int k = 0; k < specials * 4; ++k) odd |= bad[(slot * kMaxSpecial + max(x.t0 - x.special, 0)) * 4 + k];
+      // the keys among this lane's tiles whose values are not all finite (the other lane's tiles may not have been looked through)
+      const int specials = max(0, x.t0 + n - max(x.t0, x.special));
+      const uint32_t* const odd_at = bad + (slot * kMaxSpecial + max(x.t0 - x.special, 0)) * 4;
+      uint32_t odd = 0;
+      for (int k = 0; k < specials * 4; ++k) odd |= odd_at[k];
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
@@ -525,11 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
-        if (odd && n > 0) {
+        if (odd) {
 #pragma unroll 1
           for (int t = 0; t < specials * kKeys; ++t) {
             const int64_t key = (int64_t)max(x.t0, x.special) * kKeys + t;
-            if (!(bad[(slot * kMaxSpecial + max(x.t0 - x.special, 0)) * 4 + (t >> 5)] >> (t & 31) & 1) || key >= vis) continue;
+            if (!(odd_at[t >> 5] >> (t & 31) & 1) || key >= vis) continue;
             const __nv_bfloat16* v = a.v + (x.s.k0 + key) * a.v_ts + x.g * a.v_hs + 32 * c;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
@@ -539,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!real) continue;
-        if (a.splits > 1 || a.out_f32) {
-          float4* dst = reinterpret_cast<float4*>((a.splits > 1 ? a.part_o + (x.split * rows + rh) * kHeadV : static_cast<float*>(a.out) + rh * kHeadV) + 32 * c);
+        if (x.part >= 0 || a.out_f32) {
+          float4* dst = reinterpret_cast<float4*>((x.part >= 0 ? a.part_o + part * kHeadV : static_cast<float*>(a.out) + rh * kHeadV) + 32 * c);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else {
@@ -554,79 +698,212 @@ __global__ void __launch_bounds__(kThreads, 1)
       blocks += kTileBlocks * unit_tiles;
       tc_fence_before();  // (the reads of O are done before the next unit's first P is announced)
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarUnitEmpty + slot));
+      if (lane == 0) mbar_arrive(bar(L::unit_empty + slot));
     }
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  if (warp == L::mma_warp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-// The (sequence, row tile) entries of a batch in the order of their tiles of keys, most first: a counting sort by one CTA.
+// The (sequence, row tile) entries of a batch, by one CTA.
 constexpr int kListThreads = 1024, kBins = 2048;
-__global__ void __launch_bounds__(kListThreads) prompt_list_kernel(const PromptArgs a) {
-  __shared__ int32_t bins[kBins];
-  __shared__ int32_t sums[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t most = (int32_t)(((int64_t)a.max_k + kKeys - 1) / kKeys);
-  int shift = 0;
-  while ((most >> shift) >= kBins) ++shift;
-  const auto each = [&](auto use) {
-    for (int b = warp; b < a.B; b += kListThreads / 32) {
-      const PromptSeq s = load_seq(a, b);
-      const int32_t tiles = (int32_t)(((int64_t)s.m + a.rows_per_unit - 1) / a.rows_per_unit);
-      for (int32_t t = lane; t < tiles; t += 32) {
-        const int32_t last = min((int64_t)s.m, ((int64_t)t + 1) * a.rows_per_unit) - 1;
-        const int32_t cost = (int32_t)(((int64_t)visible(a, s, last) + kKeys - 1) / kKeys);
-        use(b, t, kBins - 1 - (cost >> shift));
-      }
+constexpr int kAlone = 4;  // a thread deals with a sequence of so many row tiles alone, a warp with a longer one
+
+// Calls use(sequence, row tile, tiles of keys) for every entry.
+template <class Use>
+__device__ __forceinline__ void each_entry(const PromptArgs& a, Use use) {
+  const int lane = threadIdx.x & 31;
+  for (int b0 = threadIdx.x - lane; b0 < a.B; b0 += kListThreads) {
+    PromptSeq s = {0, 0, 0, 0};
+    if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
+    const int64_t rows = (int64_t)s.m << a.pack_log;
+    const int32_t n = (int32_t)((rows + a.rows_per_unit - 1) / a.rows_per_unit);
+    if (n <= kAlone)
+      for (int32_t t = 0; t < n; ++t) use(b0 + lane, t, tiles_of(a, s, min(rows, ((int64_t)t + 1) * a.rows_per_unit)));
+    for (uint32_t left = __ballot_sync(0xffffffffu, n > kAlone); left; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      PromptSeq o;
+      o.q0 = o.k0 = 0;
+      o.m = __shfl_sync(0xffffffffu, s.m, l);
+      o.n = __shfl_sync(0xffffffffu, s.n, l);
+      const int64_t o_rows = (int64_t)o.m << a.pack_log;
+      const int32_t o_n = (int32_t)((o_rows + a.rows_per_unit - 1) / a.rows_per_unit);
+      for (int32_t t = lane; t < o_n; t += 32) use(b0 + l, t, tiles_of(a, o, min(o_rows, ((int64_t)t + 1) * a.rows_per_unit)));
     }
-  };
-  for (int i = threadIdx.x; i < kBins; i += kListThreads) bins[i] = 0;
-  __syncthreads();
-  each([&](int, int, int bin) { atomicAdd(&bins[bin], 1); });
-  __syncthreads();
-  // exclusive prefix sums of the bins, two a thread
-  const int32_t c0 = bins[2 * threadIdx.x], c1 = bins[2 * threadIdx.x + 1];
-  int32_t inc = c0 + c1;
+  }
+}
+// Exclusive prefix sum over the block's threads, and the sum of all (sums: 32 numbers of shared memory).
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* sums, T& all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int32_t up = __shfl_up_sync(0xffffffffu, inc, d);
+    const T up = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += up;
   }
+  __syncthreads();
   if (lane == 31) sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int32_t v = sums[lane];
+    T x = sums[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int32_t up = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += up;
+      const T up = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += up;
     }
-    sums[lane] = v;
+    sums[lane] = x;
   }
   __syncthreads();
-  const int32_t before = inc - c0 - c1 + (warp ? sums[warp - 1] : 0), all = sums[31];
+  all = sums[31];
+  return inc - v + (warp ? sums[warp - 1] : 0);
+}
+
+// Longest first: a counting sort by tiles of keys.
+__global__ void __launch_bounds__(kListThreads) prompt_list_kernel(const PromptArgs a) {
+  __shared__ int32_t bins[kBins];
+  __shared__ int32_t sums[32];
+  const int64_t most = ((int64_t)a.max_k + kKeys - 1) / kKeys;
+  int shift = 0;
+  while ((most >> shift) >= kBins) ++shift;
+  for (int i = threadIdx.x; i < kBins; i += kListThreads) bins[i] = 0;
+  __syncthreads();
+  each_entry(a, [&](int, int, int32_t tiles) { atomicAdd(&bins[kBins - 1 - (tiles >> shift)], 1); });
+  __syncthreads();
+  const int32_t c0 = bins[2 * threadIdx.x], c1 = bins[2 * threadIdx.x + 1];
+  int32_t all;
+  const int32_t before = block_scan(c0 + c1, sums, all);
   bins[2 * threadIdx.x] = before;
   bins[2 * threadIdx.x + 1] = before + c0;
   __syncthreads();
-  each([&](int b, int t, int bin) {
-    const int32_t at = atomicAdd(&bins[bin], 1);
+  each_entry(a, [&](int b, int t, int32_t tiles) {
+    const int32_t at = atomicAdd(&bins[kBins - 1 - (tiles >> shift)], 1);
     if (at < a.entries) a.list[at] = make_int2(b, t);
   });
   for (int64_t i = all + threadIdx.x; i < a.entries; i += kListThreads) a.list[i] = make_int2(-1, 0);
 }
+static_assert(kBins == 2 * kListThreads, "two bins a thread");
+
+// In order, for a shared call, and where each CTA's share begins (behind those: the share, and all units of work).
+__global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const PromptArgs a) {
+  __shared__ int64_t sums[32];
+  __shared__ unsigned long long work;
+  const int heads = a.virtual_heads;
+  if (threadIdx.x == 0) work = 0;
+  __syncthreads();
+  int64_t mine = 0;
+  each_entry(a, [&](int, int, int32_t tiles) { mine += cost_of(tiles); });
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&work, (unsigned long long)mine);
+  __syncthreads();
+  const int64_t total = (int64_t)work * heads, share = max((int64_t)kLeastShare + kUnitCost, (total + a.ctas - 1) / a.ctas);
+  if (threadIdx.x == 0) {
+    a.starts[a.ctas].offset = share;
+    a.starts[a.ctas + 1].offset = total;
+  }
+  for (int64_t c = threadIdx.x; c < a.ctas; c += kListThreads)
+    if (c * share >= total) a.starts[c].entry = -1;
+  // sequences in blocks of kListThreads: the entries and the work before a thread's sequence, then its own entries
+  const int lane = threadIdx.x & 31;
+  const auto write = [&](int b, int64_t t, int64_t e, int64_t w, int64_t cost) {
+    const int64_t lo = w * heads, hi = lo + cost * heads;
+    if (e < a.entries) a.list[e] = make_int2(b, (int)t);
+    for (int64_t c = (lo + share - 1) / share; c * share < hi; ++c) {
+      a.starts[c].entry = (int32_t)e;
+      a.starts[c].head = (int32_t)((c * share - lo) / cost);
+      a.starts[c].offset = (c * share - lo) % cost;
+    }
+  };
+  int64_t entry0 = 0, work0 = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kListThreads) {
+    const int b = b0 + threadIdx.x;
+    PromptSeq s = {0, 0, 0, 0};
+    if (b < a.B) s = load_seq(a, b);
+    const int64_t n = (((int64_t)s.m << a.pack_log) + a.rows_per_unit - 1) / a.rows_per_unit;
+    const auto cost = [&](const PromptSeq& o, int64_t t) {
+      return cost_of(tiles_of(a, o, min((int64_t)o.m << a.pack_log, (t + 1) * a.rows_per_unit)));
+    };
+    const auto of_lane = [&](int l) {
+      PromptSeq o = {0, 0, 0, 0};
+      o.m = __shfl_sync(0xffffffffu, s.m, l);
+      o.n = __shfl_sync(0xffffffffu, s.n, l);
+      return o;
+    };
+    const uint32_t longer = __ballot_sync(0xffffffffu, n > kAlone);
+    int64_t own = 0, entries, works;
+    if (n <= kAlone)
+      for (int64_t t = 0; t < n; ++t) own += cost(s, t);
+    for (uint32_t left = longer; left; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const PromptSeq o = of_lane(l);
+      const int64_t o_n = __shfl_sync(0xffffffffu, n, l);
+      int64_t sum = 0;
+      for (int64_t t = lane; t < o_n; t += 32) sum += cost(o, t);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == l) own = sum;
+    }
+    const int64_t e = entry0 + block_scan(n, sums, entries);
+    int64_t w = work0 + block_scan(own, sums, works);
+    if (n <= kAlone)
+      for (int64_t t = 0; t < n; ++t) {
+        const int64_t c = cost(s, t);
+        write(b, t, e + t, w, c);
+        w += c;
+      }
+    for (uint32_t left = longer; left; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const PromptSeq o = of_lane(l);
+      const int64_t o_n = __shfl_sync(0xffffffffu, n, l), o_e = __shfl_sync(0xffffffffu, e, l);
+      int64_t o_w = __shfl_sync(0xffffffffu, w, l);
+      for (int64_t t0 = 0; t0 < o_n; t0 += 32) {
+        const int64_t c = t0 + lane < o_n ? cost(o, t0 + lane) : 0;
+        int64_t inc = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+          if (lane >= d) inc += up;
+        }
+        if (c) write(b0 + (int)(threadIdx.x & ~31u) + l, t0 + lane, o_e + t0 + lane, o_w + inc - c, c);
+        o_w += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    entry0 += entries;
+    work0 += works;
+  }
+}
 
 bool encode(EncodeTiledFn enc, CUtensorMap* map, const void* p, int64_t dims, int64_t heads, int64_t head_stride, int64_t rows,
-            int64_t row_stride, int box_rows) {
+            int64_t row_stride, int box_heads, int box_rows) {
   // (a dim of one element may have any stride in the caller's tensor)
   const cuuint64_t size[3] = {(cuuint64_t)dims, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t stride[2] = {(cuuint64_t)(heads > 1 ? head_stride : dims) * 2, (cuuint64_t)(rows > 1 ? row_stride : dims) * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool ONE>
+cudaError_t launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& kr, const CUtensorMap& v,
+                   cudaStream_t stream) {
+  using L = Layout<ONE>;
+  const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.ctas);
+  cfg.blockDim = dim3(L::threads);
+  cfg.dynamicSmemBytes = L::bytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prompt_tc_kernel<ONE>, a, q, k, kr, v);
 }
 
 }  // namespace
@@ -637,31 +914,18 @@ cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream) {
   const int64_t hk = a.H / a.group;
   // without keys nothing is loaded through these three: the queries' tensor stands in for them
   const bool keys = a.num_k > 0;
-  if (!enc || !encode(enc, &q, a.q, kHeadQ, a.H, a.q_hs, a.num_q, a.q_ts, kRows) ||
-      !(keys ? encode(enc, &k, a.k, kNope, hk, a.k_hs, a.num_k, a.k_ts, kKeys) : (k = q, true)) ||
-      !(keys ? encode(enc, &kr, a.kr, kDRope, 1, 0, a.num_k, a.kr_ts, kKeys) : (kr = q, true)) ||
-      !(keys ? encode(enc, &v, a.v, kHeadV, hk, a.v_hs, a.num_k, a.v_ts, kKeys / 2) : (v = q, true)))
+  if (!enc || !encode(enc, &q, a.q, kHeadQ, a.H, a.q_hs, a.num_q, a.q_ts, a.pack, kRows / a.pack) ||
+      !(keys ? encode(enc, &k, a.k, kNope, hk, a.k_hs, a.num_k, a.k_ts, 1, kKeys) : (k = q, true)) ||
+      !(keys ? encode(enc, &kr, a.kr, kDRope, 1, 0, a.num_k, a.kr_ts, 1, kKeys) : (kr = q, true)) ||
+      !(keys ? encode(enc, &v, a.v, kHeadV, hk, a.v_hs, a.num_k, a.v_ts, 1, kKeys / 2) : (v = q, true)))
     return cudaErrorInvalidValue;
-  const int64_t units = a.entries * a.splits * a.H;
-  if (units > 0x7fffffff) return cudaErrorInvalidValue;
   if (a.listed) {
-    prompt_list_kernel<<<1, kListThreads, 0, stream>>>(a);
+    if (a.shared) prompt_share_kernel<<<1, kListThreads, 0, stream>>>(a);
+    else prompt_list_kernel<<<1, kListThreads, 0, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)units);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_tc_kernel, a, q, k, kr, v);
+  return a.rows_per_unit > kRows ? launch<false>(a, q, k, kr, v, stream) : launch<true>(a, q, k, kr, v, stream);
 }
 
 }  // namespace mla

@@ -97,20 +97,28 @@ def test_against_the_oracle(m, n, heads, group, causal, flags):
     check(p.run(causal=causal, flags=lib.MLA_FLAG_SIMT if flags == "simt" else 0), p.want(causal))
 
 
-@pytest.mark.parametrize("flags", ["simt", "tc"])
-@pytest.mark.parametrize("splits", [1, 2, 3, 7, 40])
-def test_any_number_of_parts(splits, flags):
+@pytest.mark.parametrize("m,n,heads,group", [([70, 300, 1, 0, 40], [900, 300, 515, 3, 2], 2, 2), ([700], [2500], 3, 1),
+                                             ([5, 60, 1, 2], [1300, 64, 2000, 700], 2, 1), ([2000], [2000], 2, 1), ([90, 40], [1000, 3], 8, 8)])
+@pytest.mark.parametrize("ctas", [1, 2, 3, 7, 40, 500])
+def test_shared_by_any_number_of_ctas(ctas, m, n, heads, group):
     import speculative_decode_mla_gb300 as lib
-    p = Problem([70, 300, 1, 0, 40], [900, 300, 515, 3, 2], 2, 2, seed=4)
-    f = lib.MLA_FLAG_SIMT if flags == "simt" else 0
+    p = Problem(m, n, heads, group, seed=4)
     for causal in (True, False):
-        check(p.run(num_splits=splits, flags=f, causal=causal), p.want(causal))
-    check(p.run(num_splits=splits, flags=f, out_dtype=lib.MLA_DTYPE_F32), p.want(), f32=True)
+        check(p.run(num_ctas=ctas, causal=causal), p.want(causal))
+    check(p.run(num_ctas=ctas, out_dtype=lib.MLA_DTYPE_F32), p.want(), f32=True)
+
+
+@pytest.mark.parametrize("heads,group", [(6, 3), (8, 8), (32, 32), (128, 128), (10, 5), (16, 4)])
+def test_grouped_heads(heads, group):
+    p = Problem([3, 70, 1], [50, 200, 140], heads, group, seed=heads)
+    for ctas in (0, 5):
+        for causal in (True, False):
+            check(p.run(num_ctas=ctas, causal=causal), p.want(causal))
 
 
 @pytest.mark.parametrize("flags", ["simt", "tc"])
-@pytest.mark.parametrize("splits", [0, 1, 3])
-def test_rows_outside_the_sequences_are_left_alone(splits, flags):
+@pytest.mark.parametrize("ctas", [0, 1, 3])
+def test_rows_outside_the_sequences_are_left_alone(ctas, flags):
     """Rows before the first and behind the last sequence: not written, and NaN and infinities there reach nothing."""
     import torch
     import speculative_decode_mla_gb300 as lib
@@ -120,23 +128,23 @@ def test_rows_outside_the_sequences_are_left_alone(splits, flags):
         t[:lo], t[hi:] = float("nan"), float("inf")
     out = torch.full((p.q.shape[0], 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((p.q.shape[0], 2), 7.0, device="cuda")
-    got = p.run(out=out, lse=lse, num_splits=splits, flags=lib.MLA_FLAG_SIMT if flags == "simt" else 0)
+    got = p.run(out=out, lse=lse, num_ctas=ctas, flags=lib.MLA_FLAG_SIMT if flags == "simt" else 0)
     assert got[0] is out and got[1] is lse
     check(got, clean)
     for t in (out, lse):
         assert (t[:3] == 7).all() and (t[173:] == 7).all()
 
 
-@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("what", ["k", "kr", "v"])
 @pytest.mark.parametrize("m,n,at", [([300], [300], [(0, 150)]), ([300], [300], [(0, 0)]), ([300], [400], [(0, 399), (0, 300), (0, 130)]),
                                     ([129], [129], [(0, 128)]), ([100, 60, 200], [100, 60, 200], [(1, 0), (1, 59), (0, 99), (2, 127)]),
                                     ([64], [512], [(0, 460)])])
-def test_what_a_row_does_not_see_does_not_reach_it(m, n, at, what, splits):
+def test_what_a_row_does_not_see_does_not_reach_it(m, n, at, what, ctas):
     """NaN and infinities in keys and values: rows that see them are not finite where they are not, all others as without them."""
     import torch
     p = Problem(m, n, 2, seed=6)
-    good = p.run(num_splits=splits)
+    good = p.run(num_ctas=ctas)
     odd = [float("nan"), float("inf"), float("-inf")]
     for i, (b, t) in enumerate(at):
         row = int(p.cu_k[b]) + t
@@ -147,7 +155,7 @@ def test_what_a_row_does_not_see_does_not_reach_it(m, n, at, what, splits):
             p.kv[row, i % 2, 7 * i] = float("nan")
         else:
             p.rows[row, 512 + i] = float("nan")
-    got = p.run(num_splits=splits)
+    got = p.run(num_ctas=ctas)
     out, want = values(got[0]), values(good[0])
     touched = np.zeros(out.shape, bool)
     for i, (b, t) in enumerate(at):
@@ -166,12 +174,12 @@ def test_what_a_row_does_not_see_does_not_reach_it(m, n, at, what, splits):
         assert np.array_equal(np.isnan(out), np.isnan(o)) and np.array_equal(out[np.isinf(out)], o[np.isinf(out)])
 
 
-@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("ctas", [1, 3])
 @pytest.mark.parametrize("scale", [8.0, 3e4, 1e9])
-def test_large_scores(scale, splits):
+def test_large_scores(scale, ctas):
     """Queries so large that the softmax picks one key: out is its value, or a mean of keys whose scores are equal in float32."""
     p = Problem([150], [420], 2, seed=7, scale=scale)
-    out, lse = (values(t) for t in p.run(num_splits=splits))
+    out, lse = (values(t) for t in p.run(num_ctas=ctas))
     o, l, _, size = p.want()
     ok = np.abs(out - o).max(-1) <= 0.02
     q, k = values(p.q), np.concatenate([values(p.k), np.repeat(values(p.kr)[:, None], 2, 1)], 2)
@@ -191,8 +199,8 @@ def test_growing_maxima():
     p = Problem([260], [1500], 2, seed=8)
     t = torch.arange(1500, device="cuda").float()
     p.kv[:, :, :128] *= (0.2 + t / 300)[:, None, None].to(torch.bfloat16)
-    check(p.run(num_splits=1), p.want())
-    check(p.run(num_splits=4), p.want())
+    check(p.run(num_ctas=1), p.want())
+    check(p.run(num_ctas=4), p.want())
 
 
 @pytest.mark.parametrize("layout", ["heads_first", "wide", "one"])
@@ -215,16 +223,16 @@ def test_strides(layout):
 
 
 def test_results_do_not_depend_on_the_batch():
-    """A sequence alone and among others: the same bits (with one part), whatever order the units run in; and twice the same bits."""
+    """A sequence alone and among others: the same bits (with whole units), whatever order the units run in; and twice the same bits."""
     import torch
     m = [300, 1, 700, 64, 129, 31, 256, 999, 2]
     p = Problem(m, m, 3, seed=10)
-    a, b = p.run(num_splits=1), p.run(num_splits=1)
+    a, b = p.run(num_ctas=1), p.run(num_ctas=1)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     import speculative_decode_mla_gb300 as lib
     for i in range(len(m)):
         lo, hi = int(p.cu_q[i]), int(p.cu_q[i + 1])
-        out, lse = lib.prompt_attn(p.q[lo:hi], p.k[lo:hi], p.kr[lo:hi], p.v[lo:hi], ints([0, m[i]]), max_q_len=m[i], num_splits=1)
+        out, lse = lib.prompt_attn(p.q[lo:hi], p.k[lo:hi], p.kr[lo:hi], p.v[lo:hi], ints([0, m[i]]), max_q_len=m[i], num_ctas=1)
         assert torch.equal(out, a[0][lo:hi]) and torch.equal(lse, a[1][lo:hi])
 
 
@@ -252,12 +260,12 @@ def test_lengths_are_read_on_the_device():
     cu_q, cu_k = ints(p.cu_q), ints(p.cu_k)
     desc_out, lse = torch.zeros(450, 2, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(450, 2, device="cuda")
     call = lambda **kw: lib.prompt_attn(p.q, p.k, p.kr, p.v, cu_q, cu_k, max_q_len=300, max_k_len=500, **kw)
-    for splits in (0, 1, 3):
-        call(num_splits=splits)
+    for ctas in (0, 1, 3):
+        call(num_ctas=ctas)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            call(num_splits=splits, out=desc_out, lse=lse)
+            call(num_ctas=ctas, out=desc_out, lse=lse)
         for m, n in (([200, 90, 160], [260, 90, 400]), ([1, 300, 2], [1, 310, 400]), ([0, 0, 5], [200, 50, 500])):
             cu_q.copy_(ints(ends(m)))
             cu_k.copy_(ints(ends(n)))
@@ -298,7 +306,7 @@ def test_debug_checks_report_bad_ends():
             lib.prompt_attn(p.q, p.k, p.kr, p.v, ints(cu_q), ints(cu_k), max_q_len=most, max_k_len=60, **kw)
         assert int(status) == lib.CHECK_BAD_LENGTH
         lib.prompt_attn(p.q, p.k, p.kr, p.v, ints(cu_q), ints(cu_k), max_q_len=most, max_k_len=60)  # clamped, no fault
-        lib.prompt_attn(p.q, p.k, p.kr, p.v, ints(cu_q), ints(cu_k), max_q_len=most, max_k_len=60, num_splits=2)
+        lib.prompt_attn(p.q, p.k, p.kr, p.v, ints(cu_q), ints(cu_k), max_q_len=most, max_k_len=60, num_ctas=2)
     torch.cuda.synchronize()
 
 
@@ -326,7 +334,7 @@ def test_wrapper_refuses():
                 dict(out=torch.zeros(5, 4, 128, device="cuda")), dict(lse=torch.zeros(4, 5, device="cuda")), dict(k_nope=p.k.half())):
         with pytest.raises(ValueError):
             lib.prompt_attn(**{**good, **bad})
-    for bad in (dict(k_nope=p.k[:, :1].expand(-1, 3, -1), v=p.v[:, :1].expand(-1, 3, -1)), dict(max_q_len=-1), dict(num_splits=2000), dict(softmax_scale=0.0),
+    for bad in (dict(k_nope=p.k[:, :1].expand(-1, 3, -1), v=p.v[:, :1].expand(-1, 3, -1)), dict(max_q_len=-1), dict(num_ctas=2000), dict(softmax_scale=0.0),
                 dict(q=p.q[:, :1].expand(-1, 4, -1)), dict(flags=64), dict(k_rope=torch.zeros(5, 65, dtype=torch.bfloat16, device="cuda")[:, 1:])):
         with pytest.raises(lib.MLAError):
             lib.prompt_attn(**{**good, **bad})

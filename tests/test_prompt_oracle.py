@@ -84,7 +84,7 @@ def test_expanded_and_absorbed_attention_agree():
 # ---------------------------------------------------------------------------------------------- plans
 
 def prompt_desc(**kw):
-    base = dict(num_seqs=1, num_heads=8, num_kv_heads=8, max_q_len=1000, max_k_len=1000, causal=1, out_dtype=0, flags=0, num_splits=0,
+    base = dict(num_seqs=1, num_heads=8, num_kv_heads=8, max_q_len=1000, max_k_len=1000, causal=1, out_dtype=0, flags=0, num_ctas=0,
                 softmax_scale=0.07, num_q=1000, num_k=1000, q_token_stride=8 * 192, q_head_stride=192, k_token_stride=8 * 256,
                 k_head_stride=256, k_rope_token_stride=576, v_token_stride=8 * 256, v_head_stride=256)
     base.update(kw)
@@ -93,31 +93,34 @@ def prompt_desc(**kw):
 
 @pytest.mark.parametrize("kw", [dict(), dict(max_q_len=1, num_q=1, num_k=100000, max_k_len=100000), dict(num_seqs=4096, num_q=4096, max_q_len=1),
                                 dict(num_q=1 << 20, num_k=1 << 20, max_q_len=1 << 20, max_k_len=1 << 20, num_heads=128, num_kv_heads=8),
-                                dict(num_seqs=31, num_q=5000, num_k=77777, max_q_len=5000, max_k_len=70000), dict(num_splits=7), dict(num_q=0, num_k=0),
-                                dict(max_q_len=0), dict(max_k_len=0), dict(num_splits=1024), dict(flags=2), dict(flags=2, num_splits=3)])
+                                dict(num_seqs=31, num_q=5000, num_k=77777, max_q_len=5000, max_k_len=70000), dict(num_ctas=7), dict(num_q=0, num_k=0),
+                                dict(max_q_len=0), dict(max_k_len=0), dict(num_ctas=1024), dict(flags=2), dict(num_kv_heads=1), dict(num_heads=12, num_kv_heads=4),
+                                dict(num_heads=256, num_kv_heads=1, num_q=300, max_q_len=1)])
 def test_plans_cover_every_row(lib, kw):
     d = prompt_desc(**kw)
     p = m.prompt_plan(d, 152)
-    rows = d.num_q * d.num_heads
-    assert 1 <= p.num_splits <= 1024 and (d.num_splits == 0 or p.num_splits == d.num_splits)
+    group = d.num_heads // d.num_kv_heads
     if d.flags & m.MLA_FLAG_SIMT:
-        assert p.kernel == 1 and p.units == rows * p.num_splits and not p.listed
+        assert p.kernel == 1 and p.ctas == d.num_q * d.num_heads and not p.listed and not p.shared and p.workspace_bytes == 0
     else:
-        assert p.kernel == 0 and p.rows_per_unit in (128, 256) and p.listed == (d.num_seqs > 1)
+        assert p.pack == (group if group in (1, 2, 4, 8, 16, 32, 64, 128) else 1)
         most = min(d.max_q_len, d.num_q)
-        entries = min(d.num_seqs * -(-most // p.rows_per_unit), d.num_q // p.rows_per_unit + d.num_seqs)
-        assert p.units == entries * d.num_heads * p.num_splits
-    need = rows * p.num_splits * (512 + 4) if p.num_splits > 1 else 0
-    assert p.workspace_bytes >= need + (8 * p.units // (d.num_heads * p.num_splits) if p.listed else 0)
+        assert p.kernel == 0 and p.rows_per_unit == (128 if most * p.pack <= 128 else 256) and p.listed == (d.num_seqs > 1)
+        entries = min(d.num_seqs * -(-most * p.pack // p.rows_per_unit), d.num_q * p.pack // p.rows_per_unit + d.num_seqs)
+        units = entries * d.num_heads // p.pack
+        assert p.ctas == ((d.num_ctas or 152) if p.shared else units)
+        assert p.shared == (units > 0 and (d.num_ctas > 0 or (units < 4 * 152 and min(d.max_k_len, d.num_k) > 4 * 128)))
+        need = p.ctas * 2 * p.rows_per_unit * (512 + 4) + 32 * p.ctas if p.shared else 0
+        assert p.workspace_bytes >= need + (8 * entries + (16 * (p.ctas + 2) if p.shared else 0) if p.listed else 0)
     assert bytes(p) == bytes(m.prompt_plan(d, 152))
 
 
 @pytest.mark.parametrize("bad", [dict(num_seqs=0), dict(num_heads=0), dict(num_kv_heads=3), dict(num_kv_heads=0), dict(max_q_len=-1),
-                                 dict(max_k_len=-1), dict(causal=2), dict(out_dtype=2), dict(flags=4), dict(num_splits=-1),
-                                 dict(num_splits=1025), dict(softmax_scale=0.0), dict(softmax_scale=float("nan")),
+                                 dict(max_k_len=-1), dict(causal=2), dict(out_dtype=2), dict(flags=4), dict(num_ctas=-1),
+                                 dict(num_ctas=1025), dict(softmax_scale=0.0), dict(softmax_scale=float("nan")),
                                  dict(softmax_scale=float("inf")), dict(num_q=-1), dict(num_k=-1), dict(q_token_stride=1537),
                                  dict(q_head_stride=0), dict(k_token_stride=4), dict(k_head_stride=-256), dict(k_rope_token_stride=0),
-                                 dict(v_token_stride=1 << 39), dict(v_head_stride=12), dict(num_q=(1 << 30) + 1), dict(num_k=1 << 31)])
+                                 dict(v_token_stride=1 << 39), dict(v_head_stride=12), dict(num_q=(1 << 30) + 1), dict(num_q=1 << 28), dict(num_k=1 << 31)])
 def test_plan_refuses(lib, bad):
     d = prompt_desc(**bad)
     assert lib.mla_prompt_plan(ctypes.byref(d), 152, ctypes.byref(m.PromptPlan())) in (-1, -2)
@@ -127,7 +130,7 @@ def test_plan_refuses(lib, bad):
 def test_strides_of_single_elements_are_not_looked_at(lib):
     d = prompt_desc(num_heads=1, num_kv_heads=1, num_q=1, num_k=1, q_token_stride=3, q_head_stride=5, k_token_stride=1, k_head_stride=0,
                     k_rope_token_stride=1, v_token_stride=7, v_head_stride=2)
-    assert m.prompt_plan(d, 152).units == 1
+    assert m.prompt_plan(d, 152).ctas == 1
 
 
 def test_attn_refuses_bad_pointers(lib):
