@@ -68,7 +68,10 @@ extern "C" int mla_prompt_plan(const mla_prompt_desc* d, int32_t num_sms, mla_pr
     p.rows_per_unit = longest_q(*d) * p.pack <= kPromptTile ? kPromptTile : kMaxUnitRows;
     p.listed = d->num_seqs > 1;
     const int64_t units = entries_of(*d, p.rows_per_unit) * (d->num_heads / p.pack);
-    p.shared = units > 0 && (d->num_ctas > 0 || (units < kSharedUnits * num_sms && tiles > kLeastShare));
+    // (the kernels count the work of shared calls in 32 bits)
+    const bool fits = units * (tiles + 1 + kUnitCost) < 0x40000000;
+    if (d->num_ctas > 0 && !fits) return MLA_ERR_UNSUPPORTED;
+    p.shared = units > 0 && fits && (d->num_ctas > 0 || (units < kSharedUnits * num_sms && tiles > kLeastShare));
     p.ctas = !p.shared ? units : d->num_ctas > 0 ? d->num_ctas : num_sms;
     if (p.shared && p.ctas > kMaxPromptCtas) p.ctas = kMaxPromptCtas;
     if (p.shared)
@@ -166,6 +169,7 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
   const int64_t in_l2 = kGroupBytes / ((d->num_k > 0 ? d->num_k : 1) * 2 * (kNope + kHeadV));
   const int64_t heads = (in_l2 > 1 ? in_l2 : 1) * (a.group / a.pack);  // virtual heads
   a.head_group = (int32_t)(heads < a.virtual_heads ? heads : a.virtual_heads);
+  a.out_32 = aligned(out, 32);
   a.out_f32 = d->out_dtype == MLA_DTYPE_F32;
   a.debug = debug ? 1 : 0;
   a.scale = d->softmax_scale;

@@ -17,8 +17,7 @@ constexpr int kUnitCost = 2, kLeastShare = 4;
 
 // Where a CTA of a shared call begins: its first entry, virtual head and tile there, or entry -1.
 struct PromptStart {
-  int32_t entry, head;
-  int64_t offset;
+  int32_t entry, head, offset, reserved;
 };
 // A unit whose last part CTA number c computed, with the first one's CTA: parts first .. c, to be merged.
 struct PromptMerge {
@@ -49,6 +48,7 @@ struct PromptArgs {
   int32_t B, H, group, max_q, max_k;
   int32_t pack, pack_log, virtual_heads;  // rows of a unit: pack heads a query; H / pack of such groups
   int32_t causal, shared, ctas, rows_per_unit, listed, head_group, out_f32, debug;
+  int32_t out_32;     // out is aligned to 32 bytes
   float scale, scale_log2;
 };
 
@@ -95,6 +95,6 @@ __device__ __forceinline__ int32_t tiles_of(const PromptArgs& a, const PromptSeq
   return (int32_t)(((int64_t)visible(a, s, (int32_t)((row1 - 1) >> a.pack_log)) + kPromptTile - 1) / kPromptTile);
 }
 // Units of work of an entry and virtual head: its tiles, at least one, and what a run costs besides.
-__device__ __forceinline__ int64_t cost_of(int32_t tiles) { return max(1, tiles) + kUnitCost; }
+__device__ __forceinline__ int32_t cost_of(int32_t tiles) { return max(1, tiles) + kUnitCost; }
 
 }  // namespace mla

@@ -18,7 +18,7 @@
 //
 //   warps 0-3 (, 4-7)  softmax of lane 0 (, 1): a thread a row; they also write O / l out
 //   next warp          TMA loads, and the units
-//   last warp          MMA issue, one thread
+//   the one after it   MMA issue
 //
 // TMEM (512 columns): two S [0, 256), two O [256, 512). Shared memory: Q, 48 KB a lane, and a ring of 16 KB blocks (8, with ONE
 // 11) which a tile's keys (three blocks of 64 dims) and values (two blocks of 64 keys) go through in the order
@@ -47,16 +47,22 @@ constexpr int kUnitWords = 24;
 template <bool ONE>
 struct Layout {
   static constexpr int lanes = ONE ? 1 : 2, slots = ONE ? 11 : 8;
-  static constexpr int load_warp = 4 * lanes, mma_warp = load_warp + 1, threads = 32 * (mma_warp + 1);
+  static constexpr int load_warp = 4 * lanes, mma_warp = load_warp + 1;
+  // Registers: two lanes take 168 a thread at launch with a third warpgroup (loads, MMAs, two warps that only fill it), which hands
+  // 80 of its own to the others: 2 x 208 + 88 = 3 x 168.
+  static constexpr int threads = ONE ? 32 * (mma_warp + 1) : 384;
+  static constexpr int softmax_regs = 208, other_regs = 88;
   static constexpr int ring = lanes * kQBytes, bars = ring + slots * kBlock;
-  static constexpr int full = 0, empty = slots, q_full = 2 * slots /*2*/, q_empty = q_full + 2 /*2*/, s = q_empty + 2 /*2*/, p = s + 2 /*2*/,
-                       o = p + 2 /*2*/, unit = o + 2 /*2*/, unit_empty = unit + 2 /*2*/, next = unit_empty + 2, drain = next + 1, num_bars = drain + 1;
-  static constexpr int answer = bars + 512;                // 16 bytes: the answer to a cancel request
-  static constexpr int units = answer + 16;                // two unit descriptions
-  static constexpr int bad = units + 2 * kUnitWords * 4;   // [2][kMaxSpecial][4] words: keys whose values are not all finite
-  static constexpr int flags = bad + 2 * kMaxSpecial * 16; // TMEM address, abort flag
-  static constexpr int bytes = flags + 16 + 1024;
-  static_assert(8 * num_bars <= 512 && bytes <= 232448 && answer % 16 == 0, "shared memory");
+  static constexpr int full = 0, empty = slots, q_full = 2 * slots /*2*/, q_empty = q_full + 2 /*2*/, s = q_empty + 2 /*2*/,
+                       p = s + 2 /*[half][buffer]*/, o = p + 4 /*2*/, unit = o + 2 /*2*/, unit_empty = unit + 2 /*2*/, next = unit_empty + 2,
+                       drain = next + 1, num_bars = drain + 1;
+  static constexpr int bar_bytes = (8 * num_bars + 15) / 16 * 16;
+  static constexpr int answer = bars + bar_bytes;              // 16 bytes: the answer to a cancel request
+  static constexpr int units = answer + 16;                    // two unit descriptions
+  static constexpr int bad = units + 2 * kUnitWords * 4;       // [2][kMaxSpecial][4] words: keys whose values are not all finite
+  static constexpr int flags = bad + 2 * kMaxSpecial * 16;     // TMEM address, abort flag
+  static constexpr int bytes = flags + 16;
+  static_assert(bytes <= 232448 && answer % 16 == 0, "shared memory");
 };
 
 #define TMEM_LD32(addr, r)                                                                                              \
@@ -112,16 +118,26 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n.reg .b64 ra, rb, rd;\nmov.b64 ra, {%2, %3};\nmov.b64 rb, {%4, %5};\nmul.rn.f32x2 rd, ra, rb;\nmov.b64 {%0, %1}, rd;\n}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Three-input maximum that is NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 32 bytes, in one piece where the place is aligned to 32.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 // A wait after an abort, for copies and MMAs that are in flight: bounded by its own clock.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
@@ -170,12 +186,12 @@ __device__ __forceinline__ void cut(const PromptArgs& a, Unit& x, int32_t t0, in
   x.tiles[1] = a.rows_per_unit > kRows && x.rows > mid ? t1 - t0 : 0;
 }
 // Unit number u of a call that is not shared (virtual heads in groups of a.head_group; in a group by row tile, then head).
-__device__ __forceinline__ Unit unit_at(const PromptArgs& a, int64_t u) {
-  const int64_t full = a.entries * a.head_group, group = u / full;
-  const int heads = min(a.head_group, a.virtual_heads - (int)group * a.head_group);
-  const int64_t rest = u - group * full, e = rest / heads;
-  const int vh = (int)group * a.head_group + (int)(rest - e * heads);
-  int b = 0, tile = (int)(a.entries - 1 - e);
+__device__ __forceinline__ Unit unit_at(const PromptArgs& a, uint32_t u) {
+  const uint32_t full = (uint32_t)a.entries * (uint32_t)a.head_group, group = u / full;  // (all units together are below 2^31)
+  const uint32_t heads = min(a.head_group, a.virtual_heads - (int)group * a.head_group);
+  const uint32_t rest = u - group * full, e = rest / heads;
+  const int vh = (int)(group * a.head_group + (rest - e * heads));
+  int b = 0, tile = (int)((uint32_t)a.entries - 1 - e);
   if (a.listed) {
     const int2 at = a.list[e];
     b = at.x;
@@ -186,10 +202,14 @@ __device__ __forceinline__ Unit unit_at(const PromptArgs& a, int64_t u) {
   return x;
 }
 
+// What a CTA of a shared call takes.
+__device__ __forceinline__ int32_t share_of(const PromptArgs& a, int32_t total) {
+  return max(kLeastShare + kUnitCost, total / a.ctas + (total % a.ctas ? 1 : 0));
+}
 // A CTA's way through its share of a shared call: entries in order, the virtual heads of an entry one after the other, each
 // cost_of(its tiles) units of work, of which the last kUnitCost stand for starting and ending it.
 struct Walk {
-  int64_t w, w_end, offset, share;  // offset: of w in the unit
+  int32_t w, w_end, offset, share;  // offset: of w in the unit (all work together is below 2^31: mla_prompt_plan)
   int32_t entry, head;
   bool first;
 };
@@ -203,38 +223,35 @@ __device__ __forceinline__ Walk walk_from(const PromptArgs& a, int c, int lane) 
     k.head = s.head;
     k.offset = s.offset;
     k.share = a.starts[a.ctas].offset;
-    k.w = (int64_t)c * k.share;
-    k.w_end = s.entry < 0 ? k.w : min(k.w + k.share, a.starts[a.ctas + 1].offset);
+    k.w = s.entry < 0 ? 0 : c * k.share;
+    k.w_end = s.entry < 0 ? 0 : k.w + min(k.share, a.starts[a.ctas + 1].offset - k.w);
     return k;
   }
   const PromptSeq s = load_seq(a, 0);
-  const int64_t rows = (int64_t)s.m << a.pack_log;
-  const int64_t n = (rows + a.rows_per_unit - 1) / a.rows_per_unit;
-  const auto cost = [&](int64_t e) { return e < n ? cost_of(tiles_of(a, s, min(rows, (e + 1) * a.rows_per_unit))) : 0; };
-  int64_t total = 0;
-  for (int64_t e = lane; e < n; e += 32) total += cost(e);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  total *= a.virtual_heads;
-  k.share = max((int64_t)kLeastShare + kUnitCost, (total + a.ctas - 1) / a.ctas);
-  k.w = min(total, c * k.share);
-  k.w_end = min(total, k.w + k.share);
+  const int32_t rows = s.m << a.pack_log, n = (rows + a.rows_per_unit - 1) / a.rows_per_unit;
+  const auto cost = [&](int32_t e) { return e < n ? cost_of(tiles_of(a, s, min(rows, (e + 1) * a.rows_per_unit))) * a.virtual_heads : 0; };
+  int32_t total = 0;
+  for (int32_t e = lane; e < n; e += 32) total += cost(e);
+  total = __reduce_add_sync(0xffffffffu, total);
+  k.share = share_of(a, total);
+  k.w = (int32_t)min((int64_t)total, (int64_t)c * k.share);
+  k.w_end = k.w + min(k.share, total - k.w);
   k.entry = -1;
-  int64_t before = 0;
-  for (int64_t e0 = 0; e0 < n && k.w < k.w_end; e0 += 32) {
-    const int64_t own = cost(e0 + lane) * a.virtual_heads;
-    int64_t inc = own;
+  int32_t before = 0;
+  for (int32_t e0 = 0; e0 < n && k.w < k.w_end; e0 += 32) {
+    const int32_t own = cost(e0 + lane);
+    int32_t inc = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+      const int32_t up = __shfl_up_sync(0xffffffffu, inc, d);
       if (lane >= d) inc += up;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + inc > k.w);
     if (past) {
       const int l = __ffs(past) - 1;
-      const int64_t in = k.w - before - __shfl_sync(0xffffffffu, inc - own, l), per = __shfl_sync(0xffffffffu, own, l) / a.virtual_heads;
-      k.entry = (int32_t)e0 + l;
-      k.head = (int32_t)(in / per);
+      const int32_t in = k.w - before - __shfl_sync(0xffffffffu, inc - own, l), per = __shfl_sync(0xffffffffu, own, l) / a.virtual_heads;
+      k.entry = e0 + l;
+      k.head = in / per;
       k.offset = in - k.head * per;
       break;
     }
@@ -255,13 +272,13 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
       tile = at.y;
     }
     x = unit_of(a, b, tile, k.head);
-    const int64_t len = max(1, x.all), off = k.offset, take = min(len - off, k.w_end - k.w);
+    const int32_t len = max(1, x.all), off = k.offset, take = min(len - off, k.w_end - k.w);
     if (off < len) {
-      cut(a, x, (int32_t)off, (int32_t)min((int64_t)x.all, off + take));
+      cut(a, x, off, min(x.all, off + take));
       if (off > 0 || take < len) x.part = 2 * c + (k.first ? 0 : 1);
       if (off > 0 && off + take == len) {
-        const int64_t begin = k.w - off;
-        merge->first = (int32_t)(begin / k.share);
+        const int32_t begin = k.w - off;
+        merge->first = begin / k.share;
         merge->slot = begin % k.share ? 1 : 0;
         merge->row0 = x.row0;
         merge->rows = min(a.rows_per_unit, x.rows - x.row0);
@@ -272,7 +289,7 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
     }
     k.first = false;
     // on to the next unit
-    k.w += len + kUnitCost - off;
+    k.w += min(len + kUnitCost - off, k.w_end - k.w);
     k.offset = 0;
     if (++k.head == a.virtual_heads) {
       k.head = 0;
@@ -290,9 +307,8 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
                      const __grid_constant__ CUtensorMap map_kr, const __grid_constant__ CUtensorMap map_v) {
   using L = Layout<ONE>;
   constexpr uint32_t kSlots = L::slots;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw), base = (raw_addr + 1023u) & ~1023u;
-  uint8_t* const smem = smem_raw + (base - raw_addr);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
   const auto bar = [&](int i) { return base + L::bars + 8u * (uint32_t)i; };
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::flags);
   volatile uint32_t* const abort_flag = tmem_slot + 1;
@@ -310,6 +326,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       mbar_init(bar(L::q_empty + i), 1);
       mbar_init(bar(L::s + i), 1);
       mbar_init(bar(L::p + i), 4);
+      mbar_init(bar(L::p + 2 + i), 4);
       mbar_init(bar(L::o + i), 1);
       mbar_init(bar(L::unit + i), 1);
       mbar_init(bar(L::unit_empty + i), 1 + 4 * L::lanes);
@@ -318,6 +335,10 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     mbar_init(bar(L::drain), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == L::load_warp && elect_one()) {
+    for (const CUtensorMap* map : {&map_q, &map_k, &map_kr, &map_v})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
   }
   if (warp == L::mma_warp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
@@ -331,8 +352,12 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
   // everything above read no global memory
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  const auto fewer_registers = [&] {
+    if (!ONE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::other_regs));
+  };
   if (warp == L::load_warp) {
     // ------------------------------------------------------------------------------ loads and units
+    fewer_registers();
     Walk walk = {};
     if (a.shared) walk = walk_from(a, blockIdx.x, lane);
     if (elect_one()) {
@@ -361,7 +386,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           x = next_part(a, walk, blockIdx.x, &merge);
           if (n_unit == 0) a.merges[blockIdx.x] = merge;
         } else if (u >= 0) {
-          x = unit_at(a, u);
+          x = unit_at(a, (uint32_t)u);
         }
         *unit_slot(slot) = x;
         mbar_arrive(bar(L::unit + slot));
@@ -420,97 +445,116 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     __syncwarp();
   } else if (warp == L::mma_warp) {
     // ------------------------------------------------------------------------------ MMA issue
-    if (elect_one()) {
-      constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_pv = instr_desc(kHeadV, 1);
-      uint32_t blocks = 0, p_uses[2] = {0, 0}, q_uses[2] = {0, 0}, tiles = 0;  // (tiles: of ONE, in all units)
-      bool issued = false;
-      const auto landed = [&](uint32_t i) { return wait_bar(bar(L::full + i % kSlots), (i / kSlots) & 1, abort_flag); };
-      const auto block_at = [&](uint32_t i) { return base + L::ring + (i % kSlots) * kBlock; };
-      // S buffer s = Q of lane r times the keys of the tile whose first block is `first`
-      const auto scores = [&](int r, int s, uint32_t first, bool last) {
-        for (int i = 0; i < 3; ++i) {
-          if (!landed(first + i)) return false;
-          const uint32_t qa = base + r * kQBytes + i * kBlock, kb = block_at(first + i);
+    // The whole warp walks along, so that descriptors and loop counts stay in uniform registers; one thread issues.
+    fewer_registers();
+    constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_pv = instr_desc(kHeadV, 1);
+    uint32_t blocks = 0, p_uses = 0, q_uses = 0, tiles = 0;  // (p_uses, q_uses: bit r is the parity of lane r; tiles: of ONE, in all units)
+    bool issued = false;
+    const auto wait = [&](int b, uint32_t parity) { return wait_warp(bar(b), parity, abort_flag); };
+    const auto landed = [&](uint32_t i) { return wait(L::full + i % kSlots, (i / kSlots) & 1); };
+    const auto block_at = [&](uint32_t i) { return base + L::ring + (i % kSlots) * kBlock; };
+    // S buffer s = Q of lane r times the keys of the tile whose first block is `first`
+    const auto scores = [&](int r, int s, uint32_t first, bool last) {
+      for (int i = 0; i < 3; ++i) {
+        if (!landed(first + i)) return false;
+        const uint64_t qa = smem_desc(base + r * kQBytes + i * kBlock, 16, 1024), kb = smem_desc(block_at(first + i), 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_smem_a(tmem + kColS + 128 * s, smem_desc(qa + kk * 32, 16, 1024), smem_desc(kb + kk * 32, 16, 1024), idesc_s,
-                       i > 0 || kk > 0);
-        }
-        issued = true;
-        mma_commit(bar(L::s + s));
-        if (last) mma_commit(bar(L::q_empty + r));
-        return true;
-      };
-      // O of lane r += P (in S buffer s) V
-      const auto values = [&](int r, int s, uint32_t first, bool begins) {
-        if (!wait_bar(bar(L::p + s), p_uses[s] & 1, abort_flag)) return false;
-        ++p_uses[s];
-        tc_fence_after();
-        for (int i = 0; i < 2; ++i) {
-          if (!landed(first + 3 + i)) return false;
-          const uint32_t vb = block_at(first + 3 + i);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_tmem_a(tmem + kColO + 128 * r, tmem + kColS + 128 * s + (i * 4 + kk) * 8, smem_desc(vb + kk * 2048, kBlock / 2, 1024),
-                       idesc_pv, !begins || i > 0 || kk > 0);
-        }
-        issued = true;
-        mma_commit(bar(L::o + r));
-        return true;
-      };
-      const auto free_blocks = [&](uint32_t first, int n) {
-        for (int i = 0; i < n; ++i) mma_commit(bar(L::empty + (first + i) % kSlots));
-      };
-      for (uint32_t n_unit = 0;; ++n_unit) {
-        const int slot = n_unit & 1;
-        if (!wait_bar(bar(L::unit + slot), (n_unit >> 1) & 1, abort_flag)) break;
-        const Unit x = *unit_slot(slot);
-        mbar_arrive(bar(L::unit_empty + slot));
-        if (!x.live) break;
-        const int n0 = x.tiles[0], n1 = x.tiles[1], n = max(n0, n1);
-        if (n == 0) continue;
-        bool ok = true;
-        if (ONE) {  // tiles take the S buffers in turn, across units too
-          ok = wait_bar(bar(L::q_full + 0), q_uses[0]++ & 1, abort_flag);
-          for (int j = 0; j < min(2, n) && ok; ++j) {
-            ok = scores(0, (tiles + j) & 1, blocks + kTileBlocks * j, j + 1 == n);
-            if (ok) free_blocks(blocks + kTileBlocks * j, 3);
+          for (int kk = 0; kk < 4; ++kk) mma_smem_a(tmem + kColS + 128 * s, qa + 2 * kk, kb + 2 * kk, idesc_s, i > 0 || kk > 0);
+          if (i == 2) {
+            mma_commit(bar(L::s + s));
+            if (last) mma_commit(bar(L::q_empty + r));
           }
-          for (int j = 0; j < n && ok; ++j) {
-            const uint32_t here = blocks + kTileBlocks * j, next = here + 2 * kTileBlocks;
-            ok = values(0, (tiles + j) & 1, here, j == 0);
-            if (ok) free_blocks(here + 3, 2);
-            if (ok && j + 2 < n) {
-              ok = scores(0, (tiles + j) & 1, next, j + 3 == n);
-              if (ok) free_blocks(next, 3);
+        }
+        __syncwarp();
+      }
+      issued = true;
+      return true;
+    };
+    // O of lane r += P (in S buffer s) V
+    const auto values = [&](int r, int s, uint32_t first, bool begins) {
+      for (int i = 0; i < 2; ++i) {  // (either half of P may be there first)
+        if (!wait(L::p + 2 * i + s, p_uses >> s & 1) || !landed(first + 3 + i)) return false;
+        tc_fence_after();
+        const uint64_t vb = smem_desc(block_at(first + 3 + i), kBlock / 2, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_tmem_a(tmem + kColO + 128 * r, tmem + kColS + 128 * s + (i * 4 + kk) * 8, vb + 128 * kk, idesc_pv, !begins || i > 0 || kk > 0);
+          if (i == 1) mma_commit(bar(L::o + r));
+        }
+        __syncwarp();
+      }
+      p_uses ^= 1u << s;
+      issued = true;
+      return true;
+    };
+    const auto free_blocks = [&](uint32_t first, int n) {
+      if (elect_one())
+        for (int i = 0; i < n; ++i) mma_commit(bar(L::empty + (first + i) % kSlots));
+      __syncwarp();
+    };
+    const auto queries = [&](int r) {
+      const bool ok = wait(L::q_full + r, q_uses >> r & 1);
+      q_uses ^= 1u << r;
+      return ok;
+    };
+    struct Tiles {
+      int32_t live, n0, n1;
+    };
+    const auto read_unit = [&](uint32_t u) {
+      const Unit* const from = unit_slot(u & 1);
+      const Tiles to = {__shfl_sync(0xffffffffu, from->live, 0), __shfl_sync(0xffffffffu, from->tiles[0], 0), __shfl_sync(0xffffffffu, from->tiles[1], 0)};
+      if (lane == 0) mbar_arrive(bar(L::unit_empty + (u & 1)));
+      return to;
+    };
+    for (uint32_t n_unit = 0;; ++n_unit) {
+      if (!wait(L::unit + (n_unit & 1), (n_unit >> 1) & 1)) break;
+      const Tiles x = read_unit(n_unit);
+      if (!x.live) break;
+      const int n = max(x.n0, x.n1);
+      bool ok = true;
+      if (ONE) {  // tiles take the S buffers in turn, across units too
+#pragma unroll 1
+        for (int j = -2; j < n && ok; ++j) {
+          const uint32_t here = blocks + kTileBlocks * j, next = here + 2 * kTileBlocks;
+          if (j == -2 && n > 0) ok = queries(0);
+          if (ok && j >= 0) ok = values(0, (tiles + j) & 1, here, j == 0);
+          if (ok && j >= 0) free_blocks(here + 3, 2);
+          if (ok && j + 2 < n) {
+            ok = scores(0, (tiles + j) & 1, next, j + 3 == n);
+            if (ok) free_blocks(next, 3);
+          }
+        }
+        tiles += n;
+      } else {
+#pragma unroll 1
+        for (int j = -1; j < n && ok; ++j) {
+          const uint32_t here = blocks + kTileBlocks * j, next = here + kTileBlocks;
+#pragma unroll 1
+          for (int r = 0; r < 2 && ok; ++r) {  // (one copy of the code for both lanes)
+            const int of_lane = r ? x.n1 : x.n0;
+            if (j >= 0 && j < of_lane) ok = values(r, r, here, j == 0);
+            if (ok && j >= 0 && r == 1) free_blocks(here + 3, 2);
+            if (ok && j + 1 < of_lane) {
+              if (j < 0) ok = queries(r);
+              ok = ok && scores(r, r, next, j + 2 == of_lane);
             }
           }
-          tiles += n;
-        } else {
-          if (n0) ok = wait_bar(bar(L::q_full + 0), q_uses[0]++ & 1, abort_flag) && scores(0, 0, blocks, n0 == 1);
-          if (ok && n1) ok = wait_bar(bar(L::q_full + 1), q_uses[1]++ & 1, abort_flag) && scores(1, 1, blocks, n1 == 1);
-          if (ok) free_blocks(blocks, 3);
-          for (int j = 0; j < n && ok; ++j) {
-            const uint32_t here = blocks + kTileBlocks * j, next = here + kTileBlocks;
-            if (j < n0) ok = values(0, 0, here, j == 0);
-            if (ok && j + 1 < n0) ok = scores(0, 0, next, j + 2 == n0);
-            if (ok && j < n1) ok = values(1, 1, here, j == 0);
-            if (ok) free_blocks(here + 3, 2);
-            if (ok && j + 1 < n1) ok = scores(1, 1, next, j + 2 == n1);
-            if (ok && j + 1 < n) free_blocks(next, 3);
-          }
+          if (ok && j + 1 < n) free_blocks(next, 3);
         }
-        if (!ok) break;
-        blocks += kTileBlocks * n;
       }
-      if (*abort_flag && issued) {
-        mma_commit(bar(L::drain));
-        drain_bar(bar(L::drain), 0);
-      }
+      if (!ok) break;
+      blocks += kTileBlocks * n;
+    }
+    if (*abort_flag && issued && elect_one()) {
+      mma_commit(bar(L::drain));
+      drain_bar(bar(L::drain), 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp < L::load_warp) {
     // ------------------------------------------------------------------------------ softmax and output
+    if (!ONE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::softmax_regs));
     const int r = warp >> 2, in_warp = (warp & 3) * 32, row = in_warp + lane;  // lane of the unit, row of the lane
     const uint32_t lanes = (uint32_t)in_warp << 16, tO = tmem + lanes + kColO + 128 * r;
     uint32_t blocks = 0, tile_uses = 0;  // ring blocks of the units before; tiles of this lane so far
@@ -518,22 +562,71 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     for (uint32_t n_unit = 0; ok; ++n_unit) {
       const int slot = n_unit & 1;
       if (!wait_warp(bar(L::unit + slot), (n_unit >> 1) & 1, abort_flag)) break;
-      const Unit x = *unit_slot(slot);
+      const Unit& x = *unit_slot(slot);
       if (!x.live) break;
-      const int n = x.tiles[r], unit_tiles = max(x.tiles[0], x.tiles[1]), other = x.tiles[r ^ 1];
+      const int n = r ? x.tiles[1] : x.tiles[0], unit_tiles = max(x.tiles[0], x.tiles[1]), other = r ? x.tiles[0] : x.tiles[1];
       const int at = x.row0 + r * kRows + row;  // this thread's row
       const bool real = at < x.rows;
       const int32_t vis = real ? visible(a, x.s, at >> a.pack_log) : 0;
+      const int t0 = x.t0, special = x.special;
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
       for (int j = 0; j < n; ++j) {
-        const int buf = ONE ? (int)(tile_uses & 1) : r;
+        const int buf = ONE ? (int)(tile_uses & 1) : r, tile = t0 + j;
         const uint32_t tS = tmem + lanes + kColS + 128 * buf;
-        if (!wait_warp(bar(L::s + buf), (ONE ? tile_uses >> 1 : tile_uses) & 1, abort_flag)) {
+        const auto scores_there = [&] { return wait_warp(bar(L::s + buf), (ONE ? tile_uses >> 1 : tile_uses) & 1, abort_flag); };
+        if (tile >= special && (r == 0 || j >= other)) {
+          // the first lane that uses the tile looks through its values: thread `row` has key `row`
+          // (Its block of the ring held a block of the tile before until lately; that this one landed is known from the scores: of the
+          // tile before, or at a unit's start of this one.)
+          const uint32_t block = blocks + kTileBlocks * j + 3 + (row >> 6);
+          if ((j == 0 && !scores_there()) || !wait_warp(bar(L::full + block % kSlots), (block / kSlots) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint4* const values = reinterpret_cast<uint4*>(smem + L::ring + (block % kSlots) * kBlock + (row & 63) * 128);
+          const auto piece = [&](int c) { return values + (c >> 3) * (kBlock / 32) + ((c + row) & 7); };
+          const bool behind = (int64_t)tile * kKeys + row >= x.s.n;
+          uint32_t top = 0;  // bits 15 and 31: some exponent is all ones
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint4 d = *piece(c);
+            top |= ((d.x & 0x7f807f80u) + 0x00800080u) | ((d.y & 0x7f807f80u) + 0x00800080u) | ((d.z & 0x7f807f80u) + 0x00800080u) |
+                   ((d.w & 0x7f807f80u) + 0x00800080u);
+          }
+          const bool odd = !behind && (top & 0x80008000u);
+          const uint32_t found = __ballot_sync(0xffffffffu, odd);
+          if (lane == 0) bad[(slot * kMaxSpecial + (tile - special)) * 4 + (warp & 3)] = found;
+          if (behind || odd) {
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              const auto keep = [&](uint32_t w) { return behind ? 0u : w & ~__vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); };
+              const uint4 d = *piece(c);
+              *piece(c) = make_uint4(keep(d.x), keep(d.y), keep(d.z), keep(d.w));
+            }
+          }
+          fence_proxy_async();
+        }
+        if (!scores_there()) {
           ok = false;
           break;
         }
         tc_fence_after();
+        if (tile >= special) {  // (a loop over TMEM: little code, which would have to come from far away)
+          const int64_t left = (int64_t)vis - (int64_t)tile * kKeys;
+          const int seen = (int)(left < 0 ? 0 : left > kKeys ? kKeys : left);
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 16) {
+            if (__all_sync(0xffffffffu, c + 16 <= seen)) continue;
+            uint32_t s[16];
+            TMEM_LD16(tS + c, s);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) s[k] = c + k < seen ? s[k] : 0xff800000u;
+            TMEM_ST16(tS + c, s);
+          }
+          tmem_wait_st();
+        }
         float p[kKeys];
         {
           uint32_t* u = reinterpret_cast<uint32_t*>(p);
@@ -545,26 +638,19 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
 #pragma unroll
           for (int k = 0; k < kKeys; ++k) asm volatile("" : "+f"(p[k]));
         }
-        const int tile = x.t0 + j;
-        if (tile >= x.special) {
-          const int64_t left = (int64_t)vis - (int64_t)tile * kKeys;
-          const int seen = (int)(left < 0 ? 0 : left > kKeys ? kKeys : left);
-#pragma unroll
-          for (int k = 0; k < kKeys; ++k) p[k] = k < seen ? p[k] : -INFINITY;
-        }
-        float top;
+        float top;  // NaN if a score is, so that the row becomes NaN
         {
           float t[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            t[c] = max3(p[c], p[8 + c], p[16 + c]);
+            t[c] = max3_nan(p[c], p[8 + c], p[16 + c]);
 #pragma unroll
-            for (int k = 24; k + 8 < kKeys; k += 16) t[c] = max3(t[c], p[k + c], p[k + 8 + c]);
-            t[c] = fmaxf(t[c], p[120 + c]);
+            for (int k = 24; k + 8 < kKeys; k += 16) t[c] = max3_nan(t[c], p[k + c], p[k + 8 + c]);
+            t[c] = max3_nan(t[c], p[120 + c], p[120 + c]);
           }
-          top = max3(max3(t[0], t[1], t[2]), max3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
+          top = max3_nan(max3_nan(t[0], t[1], t[2]), max3_nan(t[3], t[4], t[5]), max3_nan(t[6], t[7], t[7]));
         }
-        const bool grows = (top - m) * a.scale_log2 > 8.f;
+        const bool grows = (top - m) * a.scale_log2 > 8.f || top != top;
         if (__any_sync(0xffffffffu, grows)) {
           const float keep = grows ? ex2((m - top) * a.scale_log2) : 1.f;
           m = grows ? top : m;
@@ -587,58 +673,49 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
             }
           }
         }
-        const float off = m == -INFINITY ? 0.f : -m;
-        const float2 off2 = make_float2(off, off), scale2 = make_float2(a.scale_log2, a.scale_log2);
+        // (an infinite score: all weights NaN)
+        const float ref = m == -INFINITY ? 0.f : m == INFINITY ? NAN : m;
+        float ref_log2 = ref * a.scale_log2;
+        // One fma a weight, its addend the rounded maximum: where that is large its rounding error (2^-24 of it) would be one of
+        // the exponent, so there the maximum is taken away first. At 2^10 the two differ by 2^-14, less than the scores' own rounding.
+        if (__any_sync(0xffffffffu, !(fabsf(ref_log2) <= 1024.f))) {
+#pragma unroll
+          for (int k = 0; k < kKeys; k += 2) {
+            const float2 s = add2(make_float2(p[k], p[k + 1]), make_float2(-ref, -ref));
+            p[k] = s.x;
+            p[k + 1] = s.y;
+          }
+          ref_log2 = 0.f;
+        }
+        const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), off2 = make_float2(-ref_log2, -ref_log2);
         float2 sum[2] = {l, make_float2(0.f, 0.f)};
+        const auto announce = [&](int half) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::p + 2 * half + buf));
+        };
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t w[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            float2 v = mul2(add2(make_float2(p[64 * half + 2 * k], p[64 * half + 2 * k + 1]), off2), scale2);
+            float2 v = fma2(make_float2(p[64 * half + 2 * k], p[64 * half + 2 * k + 1]), scale2, off2);
             v.x = ex2(v.x);
             v.y = ex2(v.y);
             sum[k & 1] = add2(sum[k & 1], v);
             w[k] = pack_bf16(v.x, v.y);
           }
           TMEM_ST32(tS + 32 * half, w);
+          announce(half);
         }
         l = add2(sum[0], sum[1]);
-        if (tile >= x.special && (r == 0 || j >= other)) {
-          // the first lane that uses the tile looks through its values: thread `row` has key `row`
-          const uint32_t block = blocks + kTileBlocks * j + 3 + (row >> 6);
-          if (!wait_warp(bar(L::full + block % kSlots), (block / kSlots) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          uint4* const at = reinterpret_cast<uint4*>(smem + L::ring + (block % kSlots) * kBlock + (row & 63) * 128);
-          const bool behind = (int64_t)tile * kKeys + row >= x.s.n;
-          bool odd = false;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            uint4* const v = at + (c >> 3) * (kBlock / 32) + ((c + row) & 7);
-            uint4 d = *v;
-            const auto mask = [](uint32_t t) { return __vcmpeq2(t & 0x7f807f80u, 0x7f807f80u); };
-            const uint4 f = make_uint4(mask(d.x), mask(d.y), mask(d.z), mask(d.w));
-            if (behind) {
-              *v = make_uint4(0u, 0u, 0u, 0u);
-            } else if (f.x | f.y | f.z | f.w) {
-              odd = true;
-              *v = make_uint4(d.x & ~f.x, d.y & ~f.y, d.z & ~f.z, d.w & ~f.w);
-            }
-          }
-          const uint32_t found = __ballot_sync(0xffffffffu, odd);
-          if (lane == 0) bad[(slot * kMaxSpecial + (tile - x.special)) * 4 + (warp & 3)] = found;
-          fence_proxy_async();
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::p + buf));
         ++tile_uses;
       }
-      // the last product of this lane, then O / l
-      if (ok && n > 0 && !wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) ok = false;
+      // the last product of this lane, then O / l. (With two S buffers the product before it may not be over yet either, and a barrier
+      // may be asked for a phase only when the one before it is over.)
+      if (ONE && ok && n > 1) ok = wait_warp(bar(L::o + r), tile_uses & 1, abort_flag);
+      if (ok && n > 0) ok = wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag);
       const int64_t rh = (int64_t)(x.s.q0 + (at >> a.pack_log)) * a.H + x.h + (at & (a.pack - 1));
       const int64_t part = (int64_t)x.part * a.rows_per_unit + r * kRows + row;
       float* const lse_at = x.part >= 0 ? a.part_lse + part : a.lse + rh;
@@ -648,51 +725,59 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       }
       tc_fence_after();
       const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (real) *lse_at = sum == 0.f ? -INFINITY : m * a.scale + logf(sum);
+      if (real) *lse_at = sum == 0.f ? -INFINITY : m * a.scale + __logf(sum);
+      if (x.part >= 0 || a.out_f32) {
+        float* const dst = x.part >= 0 ? a.part_o + part * kHeadV : static_cast<float*>(a.out) + rh * kHeadV;
+#pragma unroll 1
+        for (int c = 0; c < kHeadV; c += 16) {
+          uint32_t o[16];
+          if (n > 0) {
+            TMEM_LD16(tO + c, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = n > 0 ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+          if (real) {
+            store32(dst + c, o, x.part >= 0 || a.out_32);
+            store32(dst + c + 8, o + 8, x.part >= 0 || a.out_32);
+          }
+        }
+      } else {
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) + rh * kHeadV;
+#pragma unroll 1
+        for (int c = 0; c < kHeadV; c += 32) {
+          uint32_t o[32], w[16];
+          if (n > 0) {
+            TMEM_LD32(tO + c, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) w[k] = n > 0 ? pack_bf16(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv) : 0u;
+          if (real) {
+            store32(dst + c, w, a.out_32);
+            store32(dst + c + 16, w + 8, a.out_32);
+          }
+        }
+      }
       // the keys among this lane's tiles whose values are not all finite (the other lane's tiles may not have been looked through)
-      const int specials = max(0, x.t0 + n - max(x.t0, x.special));
-      const uint32_t* const odd_at = bad + (slot * kMaxSpecial + max(x.t0 - x.special, 0)) * 4;
+      const int specials = max(0, t0 + n - max(t0, special));
+      const uint32_t* const odd_at = bad + (slot * kMaxSpecial + max(t0 - special, 0)) * 4;
       uint32_t odd = 0;
       for (int k = 0; k < specials * 4; ++k) odd |= odd_at[k];
+      if (odd && real) {
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        if (n > 0) {
-          TMEM_LD32(tO + 32 * c, reinterpret_cast<uint32_t*>(o));
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            asm volatile("" : "+f"(o[k]));
-            o[k] *= inv;
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        }
-        if (odd) {
+        for (int t = 0; t < specials * kKeys; ++t) {
+          const int64_t key = (int64_t)max(t0, special) * kKeys + t;
+          if (!(odd_at[t >> 5] >> (t & 31) & 1) || key >= vis) continue;
+          const __nv_bfloat16* const v = a.v + (x.s.k0 + key) * a.v_ts + x.g * a.v_hs;
 #pragma unroll 1
-          for (int t = 0; t < specials * kKeys; ++t) {
-            const int64_t key = (int64_t)max(x.t0, x.special) * kKeys + t;
-            if (!(odd_at[t >> 5] >> (t & 31) & 1) || key >= vis) continue;
-            const __nv_bfloat16* v = a.v + (x.s.k0 + key) * a.v_ts + x.g * a.v_hs + 32 * c;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float f = __bfloat162float(v[k]);
-              if (!isfinite(f)) o[k] += f;
-            }
+          for (int d = 0; d < kHeadV; ++d) {
+            const float f = __bfloat162float(v[d]);
+            if (isfinite(f)) continue;
+            if (x.part >= 0) a.part_o[part * kHeadV + d] += f;
+            else if (a.out_f32) static_cast<float*>(a.out)[rh * kHeadV + d] += f;
+            else static_cast<__nv_bfloat16*>(a.out)[rh * kHeadV + d] = __float2bfloat16_rn(__bfloat162float(static_cast<__nv_bfloat16*>(a.out)[rh * kHeadV + d]) + f);
           }
-        }
-        if (!real) continue;
-        if (x.part >= 0 || a.out_f32) {
-          float4* dst = reinterpret_cast<float4*>((x.part >= 0 ? a.part_o + part * kHeadV : static_cast<float*>(a.out) + rh * kHeadV) + 32 * c);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + rh * kHeadV + 32 * c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                                pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
         }
       }
       blocks += kTileBlocks * unit_tiles;
@@ -701,6 +786,8 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       if (lane == 0) mbar_arrive(bar(L::unit_empty + slot));
     }
     __syncwarp();
+  } else {
+    fewer_registers();
   }
   tc_fence_before();
   __syncthreads();
@@ -789,43 +876,42 @@ static_assert(kBins == 2 * kListThreads, "two bins a thread");
 
 // In order, for a shared call, and where each CTA's share begins (behind those: the share, and all units of work).
 __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const PromptArgs a) {
-  __shared__ int64_t sums[32];
-  __shared__ unsigned long long work;
+  __shared__ int32_t sums[32];
+  __shared__ int32_t work;
   const int heads = a.virtual_heads;
   if (threadIdx.x == 0) work = 0;
   __syncthreads();
-  int64_t mine = 0;
+  int32_t mine = 0;
   each_entry(a, [&](int, int, int32_t tiles) { mine += cost_of(tiles); });
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&work, (unsigned long long)mine);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&work, mine);
   __syncthreads();
-  const int64_t total = (int64_t)work * heads, share = max((int64_t)kLeastShare + kUnitCost, (total + a.ctas - 1) / a.ctas);
+  const int32_t total = work * heads, share = share_of(a, total);
   if (threadIdx.x == 0) {
     a.starts[a.ctas].offset = share;
     a.starts[a.ctas + 1].offset = total;
   }
-  for (int64_t c = threadIdx.x; c < a.ctas; c += kListThreads)
-    if (c * share >= total) a.starts[c].entry = -1;
+  for (int32_t c = threadIdx.x; c < a.ctas; c += kListThreads)
+    if ((int64_t)c * share >= total) a.starts[c].entry = -1;
   // sequences in blocks of kListThreads: the entries and the work before a thread's sequence, then its own entries
   const int lane = threadIdx.x & 31;
-  const auto write = [&](int b, int64_t t, int64_t e, int64_t w, int64_t cost) {
-    const int64_t lo = w * heads, hi = lo + cost * heads;
-    if (e < a.entries) a.list[e] = make_int2(b, (int)t);
-    for (int64_t c = (lo + share - 1) / share; c * share < hi; ++c) {
-      a.starts[c].entry = (int32_t)e;
-      a.starts[c].head = (int32_t)((c * share - lo) / cost);
+  const auto write = [&](int b, int t, int32_t e, int32_t w, int32_t cost) {
+    const int32_t lo = w * heads, hi = lo + cost * heads;
+    if (e < a.entries) a.list[e] = make_int2(b, t);
+    for (int32_t c = lo / share + (lo % share ? 1 : 0); c < a.ctas && (int64_t)c * share < hi; ++c) {
+      a.starts[c].entry = e;
+      a.starts[c].head = (c * share - lo) / cost;
       a.starts[c].offset = (c * share - lo) % cost;
     }
   };
-  int64_t entry0 = 0, work0 = 0;
+  int32_t entry0 = 0, work0 = 0;
   for (int b0 = 0; b0 < a.B; b0 += kListThreads) {
     const int b = b0 + threadIdx.x;
     PromptSeq s = {0, 0, 0, 0};
     if (b < a.B) s = load_seq(a, b);
-    const int64_t n = (((int64_t)s.m << a.pack_log) + a.rows_per_unit - 1) / a.rows_per_unit;
-    const auto cost = [&](const PromptSeq& o, int64_t t) {
-      return cost_of(tiles_of(a, o, min((int64_t)o.m << a.pack_log, (t + 1) * a.rows_per_unit)));
+    const int32_t n = ((s.m << a.pack_log) + a.rows_per_unit - 1) / a.rows_per_unit;
+    const auto cost = [&](const PromptSeq& o, int32_t t) {
+      return cost_of(tiles_of(a, o, min(o.m << a.pack_log, (t + 1) * a.rows_per_unit)));
     };
     const auto of_lane = [&](int l) {
       PromptSeq o = {0, 0, 0, 0};
@@ -834,38 +920,38 @@ __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const Prompt
       return o;
     };
     const uint32_t longer = __ballot_sync(0xffffffffu, n > kAlone);
-    int64_t own = 0, entries, works;
+    int32_t own = 0, entries, works;
     if (n <= kAlone)
-      for (int64_t t = 0; t < n; ++t) own += cost(s, t);
+      for (int32_t t = 0; t < n; ++t) own += cost(s, t);
     for (uint32_t left = longer; left; left &= left - 1) {
       const int l = __ffs(left) - 1;
       const PromptSeq o = of_lane(l);
-      const int64_t o_n = __shfl_sync(0xffffffffu, n, l);
-      int64_t sum = 0;
-      for (int64_t t = lane; t < o_n; t += 32) sum += cost(o, t);
+      const int32_t o_n = __shfl_sync(0xffffffffu, n, l);
+      int32_t sum = 0;
+      for (int32_t t = lane; t < o_n; t += 32) sum += cost(o, t);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == l) own = sum;
     }
-    const int64_t e = entry0 + block_scan(n, sums, entries);
-    int64_t w = work0 + block_scan(own, sums, works);
+    const int32_t e = entry0 + block_scan(n, sums, entries);
+    int32_t w = work0 + block_scan(own, sums, works);
     if (n <= kAlone)
-      for (int64_t t = 0; t < n; ++t) {
-        const int64_t c = cost(s, t);
+      for (int32_t t = 0; t < n; ++t) {
+        const int32_t c = cost(s, t);
         write(b, t, e + t, w, c);
         w += c;
       }
     for (uint32_t left = longer; left; left &= left - 1) {
       const int l = __ffs(left) - 1;
       const PromptSeq o = of_lane(l);
-      const int64_t o_n = __shfl_sync(0xffffffffu, n, l), o_e = __shfl_sync(0xffffffffu, e, l);
-      int64_t o_w = __shfl_sync(0xffffffffu, w, l);
-      for (int64_t t0 = 0; t0 < o_n; t0 += 32) {
-        const int64_t c = t0 + lane < o_n ? cost(o, t0 + lane) : 0;
-        int64_t inc = c;
+      const int32_t o_n = __shfl_sync(0xffffffffu, n, l), o_e = __shfl_sync(0xffffffffu, e, l);
+      int32_t o_w = __shfl_sync(0xffffffffu, w, l);
+      for (int32_t t0 = 0; t0 < o_n; t0 += 32) {
+        const int32_t c = t0 + lane < o_n ? cost(o, t0 + lane) : 0;
+        int32_t inc = c;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const int64_t up = __shfl_up_sync(0xffffffffu, inc, d);
+          const int32_t up = __shfl_up_sync(0xffffffffu, inc, d);
           if (lane >= d) inc += up;
         }
         if (c) write(b0 + (int)(threadIdx.x & ~31u) + l, t0 + lane, o_e + t0 + lane, o_w + inc - c, c);

@@ -278,6 +278,24 @@ def test_lengths_are_read_on_the_device():
             assert (desc_out[sum(m):] == 7).all()
 
 
+@pytest.mark.parametrize("m,heads", [(1, 4), (100, 1), (200, 1)])
+def test_repeated_with_cold_caches(m, heads):
+    """Some tiles a unit, with the caches swept before every call, so that loads are late: always the same bits."""
+    import torch
+    p = [Problem([m], [n], heads, heads, seed=n) for n in (300, 384, 640, 1000, 1400)] + [Problem([m] * 5, [200, 384, 900, 129, 700], heads, heads, seed=2)]
+    sweep = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    first = {}
+    for i in range(24):
+        for k, x in enumerate(p):
+            for causal in (True, False):
+                sweep.fill_(i)
+                got = x.run(num_ctas=i % 3, causal=causal)
+                was = first.setdefault((k, i % 3, causal), got)
+                assert torch.equal(got[0], was[0]) and torch.equal(got[1], was[1]), (i, k, causal)
+                if i < 3:
+                    check(got, x.want(causal))
+
+
 def test_two_streams_at_once():
     import torch
     a, b = Problem([700, 30], [700, 900], 2, seed=13), Problem([40] * 12, [333] * 12, 4, seed=14)
