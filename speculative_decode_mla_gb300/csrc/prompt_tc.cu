@@ -53,7 +53,9 @@ struct Layout {
   static constexpr int threads = ONE ? 32 * (mma_warp + 1) : 384;
   static constexpr int softmax_regs = 208, other_regs = 88;
   static constexpr int ring = lanes * kQBytes, bars = ring + slots * kBlock;
-  static constexpr int full = 0, empty = slots, q_full = 2 * slots /*2*/, q_empty = q_full + 2 /*2*/, s = q_empty + 2 /*2*/,
+  // barriers: keys and values landed (by tile, mod 4: with ONE, blocks of three tiles may be under way), freed (by group: the keys,
+  // then the values of a tile, mod 8), ...
+  static constexpr int keys = 0 /*4*/, vals = 4 /*4*/, freed = 8 /*8*/, q_full = 16 /*2*/, q_empty = q_full + 2 /*2*/, s = q_empty + 2 /*2*/,
                        p = s + 2 /*[half][buffer]*/, o = p + 4 /*2*/, unit = o + 2 /*2*/, unit_empty = unit + 2 /*2*/, next = unit_empty + 2,
                        drain = next + 1, num_bars = drain + 1;
   static constexpr int bar_bytes = (8 * num_bars + 15) / 16 * 16;
@@ -317,9 +319,10 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::slots; ++i) {
-      mbar_init(bar(L::full + i), 1);
-      mbar_init(bar(L::empty + i), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(L::freed + i), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(L::keys + i), 1);
+      mbar_init(bar(L::vals + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::q_full + i), 1);
@@ -362,13 +365,17 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     if (a.shared) walk = walk_from(a, blockIdx.x, lane);
     if (elect_one()) {
       uint32_t blocks = 0, q_loads[2] = {0, 0};  // ring blocks and query tiles loaded so far
-      const auto load_block = [&](const CUtensorMap* map, int x, int y, int z, bool value) {
-        const uint32_t slot = blocks % kSlots, use = blocks / kSlots;
-        if (use > 0 && !wait_bar(bar(L::empty + slot), (use - 1) & 1, abort_flag)) return false;
-        const uint32_t dst = base + L::ring + slot * kBlock, full = bar(L::full + slot);
-        mbar_arrive_expect_tx(full, kBlock);
-        tma_load3(dst, map, x, y, z, full);
-        if (value) tma_load3(dst + kBlock / 2, map, x + 64, y, z, full);
+      uint32_t tiles = 0, freed = 0;             // tiles, and groups of blocks known to be free again
+      // The next block of the ring, once the block that was there before is done with.
+      const auto load_block = [&](const CUtensorMap* map, int x, int y, int z, int landed, bool value) {
+        if (blocks >= kSlots) {
+          const uint32_t old = blocks - kSlots, group = 2 * (old / kTileBlocks) + (old % kTileBlocks >= 3);
+          for (; freed <= group; ++freed)
+            if (!wait_bar(bar(L::freed + (freed & 7)), (freed >> 3) & 1, abort_flag)) return false;
+        }
+        const uint32_t dst = base + L::ring + (blocks % kSlots) * kBlock;
+        tma_load3(dst, map, x, y, z, bar(landed));
+        if (value) tma_load3(dst + kBlock / 2, map, x + 64, y, z, bar(landed));
         ++blocks;
         return true;
       };
@@ -412,10 +419,15 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           return true;
         };
         for (int j = 0; j < n && ok; ++j) {
-          const int at = x.s.k0 + (x.t0 + j) * kKeys;
-          ok = load_block(&map_k, 0, x.g, at, false) && load_block(&map_k, 64, x.g, at, false) && load_block(&map_kr, 0, 0, at, false);
+          const int at = x.s.k0 + (x.t0 + j) * kKeys, keys = L::keys + (tiles & 3), vals = L::vals + (tiles & 3);
+          mbar_arrive_expect_tx(bar(keys), 3 * kBlock);
+          ok = load_block(&map_k, 0, x.g, at, keys, false) && load_block(&map_k, 64, x.g, at, keys, false) &&
+               load_block(&map_kr, 0, 0, at, keys, false);
           if (ok && j == 0) ok = load_q(0) && (ONE || load_q(1));
-          ok = ok && load_block(&map_v, 0, x.g, at, true) && load_block(&map_v, 0, x.g, at + 64, true);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(vals), 2 * kBlock);
+          ok = load_block(&map_v, 0, x.g, at, vals, true) && load_block(&map_v, 0, x.g, at + 64, vals, true);
+          ++tiles;
         }
         if (ok && !a.shared) {
           ok = wait_bar(bar(L::next), n_unit & 1, abort_flag);
@@ -436,7 +448,12 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       }
       if (*abort_flag) {  // what is in flight lands before the CTA ends
         if (next_asked) drain_bar(bar(L::next), n_unit & 1);
-        for (uint32_t i = blocks > kSlots ? blocks - kSlots : 0; i < blocks; ++i) drain_bar(bar(L::full + i % kSlots), (i / kSlots) & 1);
+        // (a tile begun but not loaded whole never completes its phase: its wait runs out)
+        for (uint32_t i = tiles > 2 ? tiles - 3 : 0; i <= tiles; ++i) {
+          if (i == tiles && blocks <= kTileBlocks * tiles) break;
+          drain_bar(bar(L::keys + (i & 3)), (i >> 2) & 1);
+          drain_bar(bar(L::vals + (i & 3)), (i >> 2) & 1);
+        }
         for (int r = 0; r < 2; ++r)
           if (q_loads[r]) drain_bar(bar(L::q_full + r), (q_loads[r] - 1) & 1);
         report(a.dev_status, a.dev_status != nullptr, MLA_CHECK_TIMEOUT);
@@ -448,50 +465,65 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     // The whole warp walks along, so that descriptors and loop counts stay in uniform registers; one thread issues.
     fewer_registers();
     constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_pv = instr_desc(kHeadV, 1);
-    uint32_t blocks = 0, p_uses = 0, q_uses = 0, tiles = 0;  // (p_uses, q_uses: bit r is the parity of lane r; tiles: of ONE, in all units)
-    bool issued = false;
+    uint32_t tiles = 0, p_uses = 0, q_uses = 0;  // (p_uses, q_uses: bit i is the parity of S buffer or lane i)
+    uint32_t keys_seen = 0, vals_seen = 0;       // tiles whose keys, values have landed: a probe of a barrier takes over a hundred cycles
+    bool issued = false;                         // even when the phase is over, so that no barrier is asked twice
     const auto wait = [&](int b, uint32_t parity) { return wait_warp(bar(b), parity, abort_flag); };
-    const auto landed = [&](uint32_t i) { return wait(L::full + i % kSlots, (i / kSlots) & 1); };
-    const auto block_at = [&](uint32_t i) { return base + L::ring + (i % kSlots) * kBlock; };
-    // S buffer s = Q of lane r times the keys of the tile whose first block is `first`
-    const auto scores = [&](int r, int s, uint32_t first, bool last) {
-      for (int i = 0; i < 3; ++i) {
-        if (!landed(first + i)) return false;
-        const uint64_t qa = smem_desc(base + r * kQBytes + i * kBlock, 16, 1024), kb = smem_desc(block_at(first + i), 16, 1024);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_smem_a(tmem + kColS + 128 * s, qa + 2 * kk, kb + 2 * kk, idesc_s, i > 0 || kk > 0);
-          if (i == 2) {
-            mma_commit(bar(L::s + s));
-            if (last) mma_commit(bar(L::q_empty + r));
-          }
-        }
-        __syncwarp();
+    const auto block_at = [&](uint32_t tile, int i) { return base + L::ring + (tile * kTileBlocks + i) % kSlots * kBlock; };
+    // S buffer s = Q of lane r times the keys of a tile
+    const auto scores = [&](int r, int s, uint32_t tile, bool last) {
+      if (tile >= keys_seen) {
+        if (!wait(L::keys + (tile & 3), (tile >> 2) & 1)) return false;
+        keys_seen = tile + 1;
       }
+      const uint32_t d = tmem + kColS + 128 * s;
+      uint64_t qa[3], kb[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        qa[i] = smem_desc(base + r * kQBytes + i * kBlock, 16, 1024);
+        kb[i] = smem_desc(block_at(tile, i), 16, 1024);
+      }
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_smem_a(d, qa[i] + 2 * kk, kb[i] + 2 * kk, idesc_s, i > 0 || kk > 0);
+        mma_commit(bar(L::s + s));
+        if (last) mma_commit(bar(L::q_empty + r));
+      }
+      __syncwarp();
       issued = true;
       return true;
     };
-    // O of lane r += P (in S buffer s) V
-    const auto values = [&](int r, int s, uint32_t first, bool begins) {
-      for (int i = 0; i < 2; ++i) {  // (either half of P may be there first)
-        if (!wait(L::p + 2 * i + s, p_uses >> s & 1) || !landed(first + 3 + i)) return false;
-        tc_fence_after();
-        const uint64_t vb = smem_desc(block_at(first + 3 + i), kBlock / 2, 1024);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_tmem_a(tmem + kColO + 128 * r, tmem + kColS + 128 * s + (i * 4 + kk) * 8, vb + 128 * kk, idesc_pv, !begins || i > 0 || kk > 0);
-          if (i == 1) mma_commit(bar(L::o + r));
-        }
-        __syncwarp();
+    // O of lane r += P (in S buffer s) V of a tile
+    const auto values = [&](int r, int s, uint32_t tile, bool begins) {
+      const uint32_t d = tmem + kColO + 128 * r, w = tmem + kColS + 128 * s;
+      const uint64_t v0 = smem_desc(block_at(tile, 3), kBlock / 2, 1024), v1 = smem_desc(block_at(tile, 4), kBlock / 2, 1024);
+      if (tile >= vals_seen) {
+        if (!wait(L::vals + (tile & 3), (tile >> 2) & 1)) return false;
+        vals_seen = tile + 1;
       }
+      if (!wait(L::p + s, p_uses >> s & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_tmem_a(d, w + kk * 8, v0 + 128 * kk, idesc_pv, !begins || kk > 0);
+      }
+      __syncwarp();
+      if (!wait(L::p + 2 + s, p_uses >> s & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_tmem_a(d, w + 32 + kk * 8, v1 + 128 * kk, idesc_pv, 1);
+        mma_commit(bar(L::o + r));
+      }
+      __syncwarp();
       p_uses ^= 1u << s;
       issued = true;
       return true;
     };
-    const auto free_blocks = [&](uint32_t first, int n) {
-      if (elect_one())
-        for (int i = 0; i < n; ++i) mma_commit(bar(L::empty + (first + i) % kSlots));
+    const auto free_group = [&](uint32_t group) {
+      if (elect_one()) mma_commit(bar(L::freed + (group & 7)));
       __syncwarp();
     };
     const auto queries = [&](int r) {
@@ -499,53 +531,45 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       q_uses ^= 1u << r;
       return ok;
     };
-    struct Tiles {
-      int32_t live, n0, n1;
-    };
-    const auto read_unit = [&](uint32_t u) {
-      const Unit* const from = unit_slot(u & 1);
-      const Tiles to = {__shfl_sync(0xffffffffu, from->live, 0), __shfl_sync(0xffffffffu, from->tiles[0], 0), __shfl_sync(0xffffffffu, from->tiles[1], 0)};
-      if (lane == 0) mbar_arrive(bar(L::unit_empty + (u & 1)));
-      return to;
-    };
     for (uint32_t n_unit = 0;; ++n_unit) {
       if (!wait(L::unit + (n_unit & 1), (n_unit >> 1) & 1)) break;
-      const Tiles x = read_unit(n_unit);
-      if (!x.live) break;
-      const int n = max(x.n0, x.n1);
+      const Unit* const from = unit_slot(n_unit & 1);
+      const int live = __shfl_sync(0xffffffffu, from->live, 0), n0 = __shfl_sync(0xffffffffu, from->tiles[0], 0),
+                n1 = __shfl_sync(0xffffffffu, from->tiles[1], 0), n = max(n0, n1);
+      if (lane == 0) mbar_arrive(bar(L::unit_empty + (n_unit & 1)));
+      if (!live) break;
       bool ok = true;
       if (ONE) {  // tiles take the S buffers in turn, across units too
 #pragma unroll 1
         for (int j = -2; j < n && ok; ++j) {
-          const uint32_t here = blocks + kTileBlocks * j, next = here + 2 * kTileBlocks;
+          const uint32_t here = tiles + j;
           if (j == -2 && n > 0) ok = queries(0);
-          if (ok && j >= 0) ok = values(0, (tiles + j) & 1, here, j == 0);
-          if (ok && j >= 0) free_blocks(here + 3, 2);
+          if (ok && j >= 0) ok = values(0, here & 1, here, j == 0);
+          if (ok && j >= 0) free_group(2 * here + 1);
           if (ok && j + 2 < n) {
-            ok = scores(0, (tiles + j) & 1, next, j + 3 == n);
-            if (ok) free_blocks(next, 3);
+            ok = scores(0, here & 1, here + 2, j + 3 == n);
+            if (ok) free_group(2 * (here + 2));
           }
         }
-        tiles += n;
       } else {
 #pragma unroll 1
         for (int j = -1; j < n && ok; ++j) {
-          const uint32_t here = blocks + kTileBlocks * j, next = here + kTileBlocks;
-#pragma unroll 1
-          for (int r = 0; r < 2 && ok; ++r) {  // (one copy of the code for both lanes)
-            const int of_lane = r ? x.n1 : x.n0;
-            if (j >= 0 && j < of_lane) ok = values(r, r, here, j == 0);
-            if (ok && j >= 0 && r == 1) free_blocks(here + 3, 2);
+          const uint32_t here = tiles + j;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int of_lane = r ? n1 : n0;
+            if (ok && j >= 0 && j < of_lane) ok = values(r, r, here, j == 0);
+            if (ok && j >= 0 && r == 1) free_group(2 * here + 1);
             if (ok && j + 1 < of_lane) {
               if (j < 0) ok = queries(r);
-              ok = ok && scores(r, r, next, j + 2 == of_lane);
+              ok = ok && scores(r, r, here + 1, j + 2 == of_lane);
             }
           }
-          if (ok && j + 1 < n) free_blocks(next, 3);
+          if (ok && j + 1 < n) free_group(2 * (here + 1));
         }
       }
       if (!ok) break;
-      blocks += kTileBlocks * n;
+      tiles += n;
     }
     if (*abort_flag && issued && elect_one()) {
       mma_commit(bar(L::drain));
@@ -557,7 +581,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     if (!ONE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::softmax_regs));
     const int r = warp >> 2, in_warp = (warp & 3) * 32, row = in_warp + lane;  // lane of the unit, row of the lane
     const uint32_t lanes = (uint32_t)in_warp << 16, tO = tmem + lanes + kColO + 128 * r;
-    uint32_t blocks = 0, tile_uses = 0;  // ring blocks of the units before; tiles of this lane so far
+    uint32_t tiles = 0, tile_uses = 0;  // tiles of the units before; tiles of this lane so far
     bool ok = true;
     for (uint32_t n_unit = 0; ok; ++n_unit) {
       const int slot = n_unit & 1;
@@ -577,10 +601,10 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         const auto scores_there = [&] { return wait_warp(bar(L::s + buf), (ONE ? tile_uses >> 1 : tile_uses) & 1, abort_flag); };
         if (tile >= special && (r == 0 || j >= other)) {
           // the first lane that uses the tile looks through its values: thread `row` has key `row`
-          // (Its block of the ring held a block of the tile before until lately; that this one landed is known from the scores: of the
-          // tile before, or at a unit's start of this one.)
-          const uint32_t block = blocks + kTileBlocks * j + 3 + (row >> 6);
-          if ((j == 0 && !scores_there()) || !wait_warp(bar(L::full + block % kSlots), (block / kSlots) & 1, abort_flag)) {
+          // (A barrier may be asked for a phase only when the one before it is over: here that of four tiles ago, whose block the tile
+          // after it has taken by now.)
+          const uint32_t here = tiles + j, block = kTileBlocks * here + 3 + (row >> 6);
+          if ((j == 0 && !scores_there()) || !wait_warp(bar(L::vals + (here & 3)), (here >> 2) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -707,14 +731,16 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
             w[k] = pack_bf16(v.x, v.y);
           }
           TMEM_ST32(tS + 32 * half, w);
+          // With two S buffers the product before the last may not be over when the last one's weights are there. It has to be before
+          // these are announced: afterwards the parity could not tell whether one more, two more or none has ended.
+          if (ONE && half == 1 && j == n - 1 && j > 0) ok = wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag);
           announce(half);
         }
+        if (!ok) break;
         l = add2(sum[0], sum[1]);
         ++tile_uses;
       }
-      // the last product of this lane, then O / l. (With two S buffers the product before it may not be over yet either, and a barrier
-      // may be asked for a phase only when the one before it is over.)
-      if (ONE && ok && n > 1) ok = wait_warp(bar(L::o + r), tile_uses & 1, abort_flag);
+      // the last product of this lane, then O / l
       if (ok && n > 0) ok = wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag);
       const int64_t rh = (int64_t)(x.s.q0 + (at >> a.pack_log)) * a.H + x.h + (at & (a.pack - 1));
       const int64_t part = (int64_t)x.part * a.rows_per_unit + r * kRows + row;
@@ -780,7 +806,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           }
         }
       }
-      blocks += kTileBlocks * unit_tiles;
+      tiles += unit_tiles;
       tc_fence_before();  // (the reads of O are done before the next unit's first P is announced)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::unit_empty + slot));
