@@ -354,7 +354,7 @@ def _on(device: int, stream):
         raise ValueError("the tensors must be on a CUDA device")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(device)
-        if torch.cuda.current_device() == device:
+        if torch._C._cuda_getDevice() == device:  # (CUDA is initialised: there is a tensor on it)
             return raw, _HERE
         return raw, torch.cuda.device(device)
     if stream.device_index != device:
@@ -450,7 +450,7 @@ def kv4_gather(pool, slots, *, out=None, debug: bool = False, dev_status=None, s
     raw, here = _on(dev, stream)
     with here:
         if out is None:
-            out = torch.empty((n, D_LATENT + D_ROPE), dtype=torch.bfloat16, device=pool.device)
+            out = _empty((n, D_LATENT + D_ROPE), (D_LATENT + D_ROPE, 1), torch.bfloat16, pool)
         else:
             _check_tensor("out", out, torch.bfloat16, (n, D_LATENT + D_ROPE), dev)
         rc = load_library().mla_kv4_gather(pool.data_ptr(), pool.shape[0], slots.data_ptr(), n, out.data_ptr(),
@@ -535,15 +535,37 @@ def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, 
     return out, lse
 
 
-def _check_heads(name: str, t, shape, device: int):
-    """A bf16 tensor [rows, heads, dims] of this shape (None: any extent) on `device` with contiguous dims, or ValueError."""
+@functools.lru_cache(maxsize=1)
+def _empty_call():
     import torch
+    return getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _empty(shape, strides, dtype, like):
+    """An uninitialised tensor on the current device, which is like's. After a launch torch.empty and its methods take 4 to 6 us on
+    the host of a GB300 (they are small and cold then); torch's own call for compiled graphs takes 1.6, where there is one."""
+    call = _empty_call()
+    if call is not None:
+        return call(shape, strides, dtype)
+    import torch
+    return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+
+
+def _check_heads(name: str, t, shape, device: int):
+    """A bf16 tensor of this shape on CUDA device `device` with contiguous dims (the last axis), or ValueError."""
+    import torch
+    if t.dtype is torch.bfloat16 and t.get_device() == device and t.shape == shape and t.stride(-1) == 1:
+        return
     if t.dtype is not torch.bfloat16 or t.get_device() != device:
         raise ValueError(f"{name} must be torch.bfloat16 on cuda:{device}: got {t.dtype} on {t.device}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}: got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"the dims of a row of {name} must be contiguous")
+    raise ValueError(f"the dims of a row of {name} must be contiguous")
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_desc(*fields):
+    return RopeDesc(*fields)
 
 
 def rope_append(pool, rows, slot_map, positions, cos_sin, *, weight=None, eps: float = 1e-6, rows_out=None,
@@ -560,33 +582,33 @@ def rope_append(pool, rows, slot_map, positions, cos_sin, *, weight=None, eps: f
     rows, and q_out without q. (Rows of new tensors whose position is -1 hold nothing.)
     """
     import torch
-    dev, n, bf16 = positions.get_device(), positions.shape[0], torch.bfloat16
+    dev, n, width, bf16 = positions.get_device(), positions.shape[0], D_LATENT + D_ROPE, torch.bfloat16
+    slots, stride, fmt, heads, dim, q_ts, q_hs, out_ts, out_hs = 0, width, MLA_POOL_NONE, 0, 0, 0, 0, 0, 0
     _check_tensor("positions", positions, torch.int32, (n,), dev)
     _check_tensor("cos_sin", cos_sin, torch.float32, (cos_sin.shape[0], D_ROPE), dev)
-    d = RopeDesc(num_rows=n, num_positions=cos_sin.shape[0], pairs=MLA_ROPE_HALVES if halves else MLA_ROPE_ADJACENT,
-                 eps=float(eps))
     if dev_status is not None:
         _check_tensor("dev_status", dev_status, torch.int32, (1,), dev)
     if rows is not None:
-        _check_heads("rows", rows, (n, D_LATENT + D_ROPE), dev)
-        d.row_stride = rows.stride(0) if n > 1 else D_LATENT + D_ROPE
+        _check_heads("rows", rows, (n, width), dev)
+        if n > 1:
+            stride = rows.stride(0)
         if weight is not None:
             _check_tensor("weight", weight, bf16, (D_LATENT,), dev)
         if pool is not None:
+            slots = pool.shape[0]
             if pool.dtype is bf16:
-                _check_tensor("pool", pool, bf16, (pool.shape[0], D_LATENT + D_ROPE), dev)
-                d.pool_format = MLA_POOL_BF16
+                _check_tensor("pool", pool, bf16, (slots, width), dev)
+                fmt = MLA_POOL_BF16
             else:
-                _check_tensor("pool", pool, torch.uint8, (pool.shape[0], KV4_ROW_BYTES), dev)
-                d.pool_format = MLA_POOL_KV4
+                _check_tensor("pool", pool, torch.uint8, (slots, KV4_ROW_BYTES), dev)
+                fmt = MLA_POOL_KV4
             if slot_map is None:
                 raise ValueError("a pool needs a slot_map")
             _check_tensor("slot_map", slot_map, torch.int32, (n,), dev)
-            d.num_slots = pool.shape[0]
         elif slot_map is not None:
             raise ValueError("a slot_map needs a pool")
         if rows_out is not None:
-            _check_tensor("rows_out", rows_out, bf16, (n, D_LATENT + D_ROPE), dev)
+            _check_tensor("rows_out", rows_out, bf16, (n, width), dev)
         elif pool is None and not want_rows:
             raise ValueError("rows need a pool or rows_out")
     elif pool is not None or slot_map is not None or weight is not None or rows_out is not None:
@@ -594,30 +616,41 @@ def rope_append(pool, rows, slot_map, positions, cos_sin, *, weight=None, eps: f
     elif q is None:
         raise ValueError("rows or q is needed")
     if q is not None:
-        _check_heads("q", q, (n, None, None), dev)
-        heads, dim = q.shape[1], q.shape[2]
-        d.num_heads, d.head_dim = heads, dim
-        d.q_token_stride, d.q_head_stride = q.stride(0) if n > 1 else heads * dim, q.stride(1) if heads > 1 else dim
+        if q.dim() != 3:
+            raise ValueError(f"q must have the shape (n, heads, dims): got {tuple(q.shape)}")
+        _, heads, dim = shape = q.shape
+        _check_heads("q", q, (n, heads, dim), dev)
+        q_ts, q_hs, _ = q.stride()
         if q_weight is not None:
             _check_tensor("q_weight", q_weight, bf16, (dim,), dev)
         if q_out is not None:
-            _check_heads("q_out", q_out, (n, heads, dim), dev)
-            d.q_out_token_stride = q_out.stride(0) if n > 1 else heads * dim
-            d.q_out_head_stride = q_out.stride(1) if heads > 1 else dim
+            _check_heads("q_out", q_out, shape, dev)
+            out_ts, out_hs, _ = q_out.stride()
+        else:
+            out_ts, out_hs = heads * dim, dim
+        if n <= 1:
+            q_ts = out_ts = heads * dim
+        if heads == 1:
+            q_hs = out_hs = dim
     elif q_weight is not None or q_out is not None:
         raise ValueError("q_weight and q_out need q")
     raw, here = _on(dev, stream)
     with here:
         if rows is not None and rows_out is None and want_rows:
-            rows_out = torch.empty((n, D_LATENT + D_ROPE), dtype=bf16, device=positions.device)
+            rows_out = _empty((n, width), (width, 1), bf16, rows)
         if q is not None and q_out is None:
-            q_out = torch.empty(tuple(q.shape), dtype=bf16, device=positions.device)
-            d.q_out_token_stride, d.q_out_head_stride = heads * dim, dim
-        rc = load_library().mla_rope_append(
-            ctypes.byref(d), _ptr_or_none(rows), _ptr_or_none(weight), _ptr_or_none(q), _ptr_or_none(q_weight),
-            positions.data_ptr(), cos_sin.data_ptr(), _ptr_or_none(slot_map), _ptr_or_none(pool), _ptr_or_none(rows_out),
-            _ptr_or_none(q_out), int(debug), _ptr_or_none(dev_status), raw)
-    _check(rc, "mla_rope_append")
+            q_out = _empty((n, heads, dim), (heads * dim, dim, 1), bf16, q)
+        # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
+        d = _rope_desc(n, stride, slots, q_ts, q_hs, out_ts, out_hs, fmt, heads, dim, cos_sin.shape[0],
+                       MLA_ROPE_HALVES if halves else MLA_ROPE_ADJACENT, float(eps))
+        rc = (_lib or load_library()).mla_rope_append(
+            d, None if rows is None else rows.data_ptr(), None if weight is None else weight.data_ptr(),
+            None if q is None else q.data_ptr(), None if q_weight is None else q_weight.data_ptr(), positions.data_ptr(),
+            cos_sin.data_ptr(), None if slot_map is None else slot_map.data_ptr(), None if pool is None else pool.data_ptr(),
+            None if rows_out is None else rows_out.data_ptr(), None if q_out is None else q_out.data_ptr(), int(debug),
+            None if dev_status is None else dev_status.data_ptr(), raw)
+    if rc:
+        _check(rc, "mla_rope_append")
     return rows_out, q_out
 
 
@@ -654,17 +687,20 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
     """
     import torch
     dev, i32, bf16 = q.get_device(), torch.int32, torch.bfloat16
-    _check_heads("q", q, (None, None, 192), dev)
-    nq, heads = q.shape[0], q.shape[1]
-    _check_heads("k_nope", k_nope, (None, None, 128), dev)
-    nk, hk = k_nope.shape[0], k_nope.shape[1]
+    if q.dim() != 3 or k_nope.dim() != 3:
+        raise ValueError(f"q and k_nope must have the shapes (n, heads, dims): got {tuple(q.shape)} and {tuple(k_nope.shape)}")
+    nq, heads, _ = q.shape
+    nk, hk, _ = shape = k_nope.shape
+    _check_heads("q", q, (nq, heads, 192), dev)
+    _check_heads("k_nope", k_nope, (nk, hk, 128), dev)
     _check_heads("k_rope", k_rope, (nk, D_ROPE), dev)
-    _check_heads("v", v, (nk, hk, 128), dev)
+    _check_heads("v", v, shape, dev)
+    ends = cu_q.shape[0]
+    _check_tensor("cu_q", cu_q, i32, (ends,), dev)
     if cu_k is None:
         cu_k = cu_q
-    B = cu_q.shape[0] - 1
-    _check_tensor("cu_q", cu_q, i32, (B + 1,), dev)
-    _check_tensor("cu_k", cu_k, i32, (B + 1,), dev)
+    else:
+        _check_tensor("cu_k", cu_k, i32, (ends,), dev)
     if dev_status is not None:
         _check_tensor("dev_status", dev_status, i32, (1,), dev)
     out_type = bf16 if out_dtype == MLA_DTYPE_BF16 else torch.float32
@@ -672,26 +708,27 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
     with here:
         # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
         desc, need = _prompt_desc(
-            dev, B, heads, hk, int(max_q_len), int(max_q_len if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
-            int(DEFAULT_FLAGS if flags is None else flags), int(num_ctas), float(softmax_scale), nq, nk, q.stride(0), q.stride(1),
-            k_nope.stride(0), k_nope.stride(1), k_rope.stride(0), v.stride(0), v.stride(1))
+            dev, ends - 1, heads, hk, int(max_q_len), int(max_q_len if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
+            int(DEFAULT_FLAGS if flags is None else flags), int(num_ctas), float(softmax_scale), nq, nk, *q.stride()[:2],
+            *k_nope.stride()[:2], k_rope.stride(0), *v.stride()[:2])
         if out is None:
-            out = torch.empty((nq, heads, 128), device=q.device, dtype=out_type)
+            out = _empty((nq, heads, 128), (heads * 128, 128, 1), out_type, q)
         else:
             _check_tensor("out", out, out_type, (nq, heads, 128), dev)
         if lse is None:
-            lse = torch.empty((nq, heads), device=q.device, dtype=torch.float32)
+            lse = _empty((nq, heads), (heads, 1), torch.float32, q)
         else:
             _check_tensor("lse", lse, torch.float32, (nq, heads), dev)
         if workspace is not None:
             _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
         elif need:
-            workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-        rc = load_library().mla_prompt_attn(
-            ctypes.byref(desc), q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
-            cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), _ptr_or_none(workspace),
-            0 if workspace is None else workspace.numel(), _ptr_or_none(dev_status), raw)
-    _check(rc, "mla_prompt_attn")
+            workspace = _empty((need,), (1,), torch.uint8, q)
+        rc = (_lib or load_library()).mla_prompt_attn(
+            desc, q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+            out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), None if dev_status is None else dev_status.data_ptr(), raw)
+    if rc:
+        _check(rc, "mla_prompt_attn")
     return out, lse
 
 

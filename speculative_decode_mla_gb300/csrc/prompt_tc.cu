@@ -30,6 +30,8 @@
 //
 // Every wait is bounded (about 2 s). On a timeout the kernel stops issuing work, drains what is in flight, reports
 // MLA_CHECK_TIMEOUT, gives its rows a NaN lse and exits.
+#include <atomic>
+
 #include "prompt.cuh"
 #include "tc.cuh"
 
@@ -1003,8 +1005,15 @@ template <bool ONE>
 cudaError_t launch(const PromptArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& kr, const CUtensorMap& v,
                    cudaStream_t stream) {
   using L = Layout<ONE>;
-  const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
-  if (e != cudaSuccess) return e;
+  // once a device (a racing second time does no harm)
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  if (dev < 0 || dev >= 64 || !set[dev].load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_relaxed);
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
