@@ -55,8 +55,8 @@ struct Layout {
   static constexpr int threads = ONE ? 32 * (mma_warp + 1) : 384;
   static constexpr int softmax_regs = 208, other_regs = 88;
   static constexpr int ring = lanes * kQBytes, bars = ring + slots * kBlock;
-  // barriers: keys and values landed (by tile, mod 4: with ONE, blocks of three tiles may be under way), freed (by group: the keys,
-  // then the values of a tile, mod 8), ...
+  // barriers: keys and values landed (by tile, mod 4: with ONE, blocks of three tiles may be under way), freed (group
+  // 2 t: the keys of tile t, group 2 t + 1: its values; mod 8), ...
   static constexpr int keys = 0 /*4*/, vals = 4 /*4*/, freed = 8 /*8*/, q_full = 16 /*2*/, q_empty = q_full + 2 /*2*/, s = q_empty + 2 /*2*/,
                        p = s + 2 /*[half][buffer]*/, o = p + 4 /*2*/, unit = o + 2 /*2*/, unit_empty = unit + 2 /*2*/, next = unit_empty + 2,
                        drain = next + 1, num_bars = drain + 1;
@@ -94,18 +94,22 @@ __host__ __device__ constexpr uint32_t instr_desc(int N, int b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(kRows >> 4) << 24);
 }
-__device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// Shared-memory descriptors with 128-byte swizzle and 1024 bytes from one group of eight rows to the next, as their low words (the
+// address, and for B read MN-major the 8 KB from one block of 64 dims to the next); the high words are all the same.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n.reg .pred p;\n.reg .b64 b;\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_smem_a(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_smem_a(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n.reg .pred p;\n.reg .b64 a, b;\nmov.b64 a, {%1, %5};\nmov.b64 b, {%2, %5};\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -142,6 +146,19 @@ __device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool whole
     static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
     static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
+}
+// Four barriers asked together, which takes the time of one: bit i, phase i is over.
+__device__ __forceinline__ uint32_t probe4(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2, uint32_t b3, uint32_t p3) {
+  uint32_t r0, r1, r2, r3;
+  asm volatile(
+      "{\n.reg .pred p, q, r, s;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%4], %5;\nmbarrier.test_wait.parity.shared::cta.b64 q, [%6], %7;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 r, [%8], %9;\nmbarrier.test_wait.parity.shared::cta.b64 s, [%10], %11;\n"
+      "selp.u32 %0, 1, 0, p;\nselp.u32 %1, 2, 0, q;\nselp.u32 %2, 4, 0, r;\nselp.u32 %3, 8, 0, s;\n}"
+      : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2), "r"(b3), "r"(p3)
+      : "memory");
+  return r0 | r1 | r2 | r3;
 }
 // A wait after an abort, for copies and MMAs that are in flight: bounded by its own clock.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
@@ -382,7 +399,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         return true;
       };
       bool next_asked = false;
-      uint32_t n_unit = 0;
+      uint32_t n_unit = 0, n_asked = 0;
       int64_t u = blockIdx.x;
       bool ok = true;
       PromptMerge merge = {};
@@ -397,8 +414,12 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         } else if (u >= 0) {
           x = unit_at(a, (uint32_t)u);
         }
-        *unit_slot(slot) = x;
-        mbar_arrive(bar(L::unit + slot));
+        // (a unit without rows, where the lengths leave fewer than the call has room for, is passed over)
+        const bool none = !a.shared && x.live && x.rows == 0;
+        if (!none) {
+          *unit_slot(slot) = x;
+          mbar_arrive(bar(L::unit + slot));
+        }
         if (!x.live) break;
         if (!a.shared) {  // ask for the unit after this one
           mbar_arrive_expect_tx(bar(L::next), 16);
@@ -432,8 +453,9 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           ++tiles;
         }
         if (ok && !a.shared) {
-          ok = wait_bar(bar(L::next), n_unit & 1, abort_flag);
+          ok = wait_bar(bar(L::next), n_asked & 1, abort_flag);
           if (!ok) break;
+          ++n_asked;
           next_asked = false;
           uint32_t got, id;
           asm volatile(
@@ -446,10 +468,10 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
               : "memory");
           u = got ? (int64_t)id : -1;
         }
-        ++n_unit;
+        if (!none) ++n_unit;
       }
       if (*abort_flag) {  // what is in flight lands before the CTA ends
-        if (next_asked) drain_bar(bar(L::next), n_unit & 1);
+        if (next_asked) drain_bar(bar(L::next), n_asked & 1);
         // (a tile begun but not loaded whole never completes its phase: its wait runs out)
         for (uint32_t i = tiles > 2 ? tiles - 3 : 0; i <= tiles; ++i) {
           if (i == tiles && blocks <= kTileBlocks * tiles) break;
@@ -464,118 +486,128 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     __syncwarp();
   } else if (warp == L::mma_warp) {
     // ------------------------------------------------------------------------------ MMA issue
-    // The whole warp walks along, so that descriptors and loop counts stay in uniform registers; one thread issues.
+    // One thread. The tensor cores hold about four MMAs (256 cycles) that have been issued and not begun, and an issue waits for room, so
+    // what this thread does between the last MMA of one step and the first of the next has to take less: a probe of a barrier takes
+    // 55 cycles (80 for a warp, with its vote), a commit about 50. So the next step's barriers are asked, all together, before the last
+    // four MMAs of a step, and O is committed only where nothing later tells the same. (A tile and a lane, all barriers long done, where
+    // the MMAs take 1280 cycles: every wait at its place, a warp, 1720; one thread, 1418; with the early probes 1398; and without O's
+    // commit the calls of one long prompt are 2% faster than with it and without the probes: 126.5 us against 129.7 at 16 heads of 4096
+    // rows and keys, not causal.)
     fewer_registers();
-    constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_pv = instr_desc(kHeadV, 1);
-    uint32_t tiles = 0, p_uses = 0, q_uses = 0;  // (p_uses, q_uses: bit i is the parity of S buffer or lane i)
-    uint32_t keys_seen = 0, vals_seen = 0;       // tiles whose keys, values have landed: a probe of a barrier takes over a hundred cycles
-    bool issued = false;                         // even when the phase is over, so that no barrier is asked twice
-    const auto wait = [&](int b, uint32_t parity) { return wait_warp(bar(b), parity, abort_flag); };
-    const auto block_at = [&](uint32_t tile, int i) { return base + L::ring + (tile * kTileBlocks + i) % kSlots * kBlock; };
-    // S buffer s = Q of lane r times the keys of a tile
-    const auto scores = [&](int r, int s, uint32_t tile, bool last) {
-      if (tile >= keys_seen) {
-        if (!wait(L::keys + (tile & 3), (tile >> 2) & 1)) return false;
-        keys_seen = tile + 1;
-      }
-      const uint32_t d = tmem + kColS + 128 * s;
-      uint64_t qa[3], kb[3];
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = instr_desc(kKeys, 0), idesc_pv = instr_desc(kHeadV, 1);
+      uint32_t tiles = 0, p_uses = 0, q_uses = 0;  // (p_uses, q_uses: bit i is the parity of S buffer or lane i)
+      uint32_t keys_seen = 0, vals_seen = 0;       // tiles whose keys, values are known to have landed
+      uint32_t p_seen = 0;                         // bits of the next step's halves of P that are known to be there
+      bool issued = false;
+      const auto wait = [&](int b, uint32_t parity) { return wait_bar(bar(b), parity, abort_flag); };
+      const auto block_at = [&](uint32_t tile, int i) { return base + L::ring + (tile * kTileBlocks + i) % kSlots * kBlock; };
+      // S buffer s = Q of lane r times the keys of a tile; `ask` asks for what comes next.
+      const auto scores = [&](int r, int s, uint32_t tile, bool last, auto ask) {
+        if (tile >= keys_seen) {
+          if (!wait(L::keys + (tile & 3), (tile >> 2) & 1)) return false;
+          keys_seen = tile + 1;
+        }
+        const uint32_t d = tmem + kColS + 128 * s;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        qa[i] = smem_desc(base + r * kQBytes + i * kBlock, 16, 1024);
-        kb[i] = smem_desc(block_at(tile, i), 16, 1024);
-      }
-      if (elect_one()) {
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t qa = desc_low(base + r * kQBytes + i * kBlock, 16), kb = desc_low(block_at(tile, i), 16);
+          if (i == 2) ask();
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_smem_a(d, qa[i] + 2 * kk, kb[i] + 2 * kk, idesc_s, i > 0 || kk > 0);
+          for (int kk = 0; kk < 4; ++kk) mma_smem_a(d, qa + 2 * kk, kb + 2 * kk, idesc_s, i > 0 || kk > 0);
+        }
         mma_commit(bar(L::s + s));
         if (last) mma_commit(bar(L::q_empty + r));
-      }
-      __syncwarp();
-      issued = true;
-      return true;
-    };
-    // O of lane r += P (in S buffer s) V of a tile
-    const auto values = [&](int r, int s, uint32_t tile, bool begins) {
-      const uint32_t d = tmem + kColO + 128 * r, w = tmem + kColS + 128 * s;
-      const uint64_t v0 = smem_desc(block_at(tile, 3), kBlock / 2, 1024), v1 = smem_desc(block_at(tile, 4), kBlock / 2, 1024);
-      if (tile >= vals_seen) {
-        if (!wait(L::vals + (tile & 3), (tile >> 2) & 1)) return false;
-        vals_seen = tile + 1;
-      }
-      if (!wait(L::p + s, p_uses >> s & 1)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_tmem_a(d, w + kk * 8, v0 + 128 * kk, idesc_pv, !begins || kk > 0);
-      }
-      __syncwarp();
-      if (!wait(L::p + 2 + s, p_uses >> s & 1)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_tmem_a(d, w + 32 + kk * 8, v1 + 128 * kk, idesc_pv, 1);
-        mma_commit(bar(L::o + r));
-      }
-      __syncwarp();
-      p_uses ^= 1u << s;
-      issued = true;
-      return true;
-    };
-    const auto free_group = [&](uint32_t group) {
-      if (elect_one()) mma_commit(bar(L::freed + (group & 7)));
-      __syncwarp();
-    };
-    const auto queries = [&](int r) {
-      const bool ok = wait(L::q_full + r, q_uses >> r & 1);
-      q_uses ^= 1u << r;
-      return ok;
-    };
-    for (uint32_t n_unit = 0;; ++n_unit) {
-      if (!wait(L::unit + (n_unit & 1), (n_unit >> 1) & 1)) break;
-      const Unit* const from = unit_slot(n_unit & 1);
-      const int live = __shfl_sync(0xffffffffu, from->live, 0), n0 = __shfl_sync(0xffffffffu, from->tiles[0], 0),
-                n1 = __shfl_sync(0xffffffffu, from->tiles[1], 0), n = max(n0, n1);
-      if (lane == 0) mbar_arrive(bar(L::unit_empty + (n_unit & 1)));
-      if (!live) break;
-      bool ok = true;
-      if (ONE) {  // tiles take the S buffers in turn, across units too
-#pragma unroll 1
-        for (int j = -2; j < n && ok; ++j) {
-          const uint32_t here = tiles + j;
-          if (j == -2 && n > 0) ok = queries(0);
-          if (ok && j >= 0) ok = values(0, here & 1, here, j == 0);
-          if (ok && j >= 0) free_group(2 * here + 1);
-          if (ok && j + 2 < n) {
-            ok = scores(0, here & 1, here + 2, j + 3 == n);
-            if (ok) free_group(2 * (here + 2));
-          }
+        issued = true;
+        return true;
+      };
+      // O of lane r += P (in S buffer s) V of a tile
+      const auto values = [&](int r, int s, uint32_t tile, bool begins, bool ends) {
+        const uint32_t d = tmem + kColO + 128 * r, w = tmem + kColS + 128 * s;
+        if (tile >= vals_seen) {
+          if (!wait(L::vals + (tile & 3), (tile >> 2) & 1)) return false;
+          vals_seen = tile + 1;
         }
-      } else {
-#pragma unroll 1
-        for (int j = -1; j < n && ok; ++j) {
-          const uint32_t here = tiles + j;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int of_lane = r ? n1 : n0;
-            if (ok && j >= 0 && j < of_lane) ok = values(r, r, here, j == 0);
-            if (ok && j >= 0 && r == 1) free_group(2 * here + 1);
-            if (ok && j + 1 < of_lane) {
-              if (j < 0) ok = queries(r);
-              ok = ok && scores(r, r, here + 1, j + 2 == of_lane);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t vb = desc_low(block_at(tile, 3 + i), kBlock / 2);
+          if (!(p_seen >> i & 1) && !wait(L::p + 2 * i + s, p_uses >> s & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_tmem_a(d, w + 32 * i + kk * 8, vb + 128 * kk, idesc_pv, !begins || i > 0 || kk > 0);
+        }
+        p_seen = 0;
+        p_uses ^= 1u << s;
+        if (ends) mma_commit(bar(L::o + r));  // (with two lanes the lane's next scores tell that the tiles before the last are in)
+        issued = true;
+        return true;
+      };
+      // P in S buffer s, the values of tile v and the keys of tile k, as far as they are there. (A barrier may be asked for a phase only
+      // when the one before it is over: P's was waited for, the tiles' was four tiles ago.)
+      const auto look = [&](int s, uint32_t v, uint32_t k) {
+        const uint32_t got = probe4(bar(L::p + s), p_uses >> s & 1, bar(L::p + 2 + s), p_uses >> s & 1, bar(L::vals + (v & 3)), (v >> 2) & 1,
+                                    bar(L::keys + (k & 3)), (k >> 2) & 1);
+        p_seen = got & 3;
+        if ((got & 4) && v == vals_seen) vals_seen = v + 1;
+        if ((got & 8) && k == keys_seen) keys_seen = k + 1;
+      };
+      // Group 2 t is the keys of tile t, group 2 t + 1 its values: done with.
+      const auto free_group = [&](uint32_t g) { mma_commit(bar(L::freed + (g & 7))); };
+      const auto queries = [&](int r) {
+        const bool ok = wait(L::q_full + r, q_uses >> r & 1);
+        q_uses ^= 1u << r;
+        return ok;
+      };
+      for (uint32_t n_unit = 0;; ++n_unit) {
+        if (!wait(L::unit + (n_unit & 1), (n_unit >> 1) & 1)) break;
+        const Unit* const x = unit_slot(n_unit & 1);
+        const int live = x->live, n0 = x->tiles[0], n1 = x->tiles[1], n = max(n0, n1);
+        mbar_arrive(bar(L::unit_empty + (n_unit & 1)));
+        if (!live) break;
+        bool ok = true;
+        if (ONE) {  // tiles take the S buffers in turn, across units too
+#pragma unroll 1
+          for (int j = -2; j < n && ok; ++j) {
+            const uint32_t here = tiles + j;
+            if (j >= 0) {
+              ok = values(0, here & 1, here, j == 0, true);
+              if (ok) free_group(2 * here + 1);
+            }
+            if (ok && j + 2 < n) {
+              if (j == -2) ok = queries(0);
+              ok = ok && scores(0, here & 1, here + 2, j + 3 == n, [&] {
+                if (j >= -1) look((here + 1) & 1, here + 1, here + 3);
+              });
+              if (ok) free_group(2 * (here + 2));
             }
           }
-          if (ok && j + 1 < n) free_group(2 * (here + 1));
+        } else {
+#pragma unroll 1
+          for (int j = -1; j < n && ok; ++j) {
+            const uint32_t here = tiles + j;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int of_lane = r ? n1 : n0;
+              if (ok && j >= 0 && j < of_lane) ok = values(r, r, here, j == 0, j + 1 == of_lane);
+              if (ok && j >= 0 && r == 1) free_group(2 * here + 1);
+              if (ok && j + 1 < of_lane) {
+                if (j < 0) ok = queries(r);
+                ok = ok && scores(r, r, here + 1, j + 2 == of_lane, [&] {
+                  // the step after this one: lane 1's with this tile, or lane 0's with the next
+                  if (r == 0 ? j >= 0 && j < n1 : j + 1 < n0) look(r ^ 1, here + r, here + r + 1);
+                });
+              }
+            }
+            if (ok && j + 1 < n) free_group(2 * (here + 1));
+          }
         }
+        if (!ok) break;
+        tiles += n;
       }
-      if (!ok) break;
-      tiles += n;
-    }
-    if (*abort_flag && issued && elect_one()) {
-      mma_commit(bar(L::drain));
-      drain_bar(bar(L::drain), 0);
+      if (*abort_flag && issued) {
+        mma_commit(bar(L::drain));
+        drain_bar(bar(L::drain), 0);
+      }
     }
     __syncwarp();
   } else if (warp < L::load_warp) {
@@ -583,7 +615,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     if (!ONE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::softmax_regs));
     const int r = warp >> 2, in_warp = (warp & 3) * 32, row = in_warp + lane;  // lane of the unit, row of the lane
     const uint32_t lanes = (uint32_t)in_warp << 16, tO = tmem + lanes + kColO + 128 * r;
-    uint32_t tiles = 0, tile_uses = 0;  // tiles of the units before; tiles of this lane so far
+    uint32_t tiles = 0, tile_uses = 0, units_done = 0;  // tiles of the units before; tiles, and units with any, of this lane so far
     bool ok = true;
     for (uint32_t n_unit = 0; ok; ++n_unit) {
       const int slot = n_unit & 1;
@@ -638,21 +670,6 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           break;
         }
         tc_fence_after();
-        if (tile >= special) {  // (a loop over TMEM: little code, which would have to come from far away)
-          const int64_t left = (int64_t)vis - (int64_t)tile * kKeys;
-          const int seen = (int)(left < 0 ? 0 : left > kKeys ? kKeys : left);
-#pragma unroll 1
-          for (int c = 0; c < kKeys; c += 16) {
-            if (__all_sync(0xffffffffu, c + 16 <= seen)) continue;
-            uint32_t s[16];
-            TMEM_LD16(tS + c, s);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) s[k] = c + k < seen ? s[k] : 0xff800000u;
-            TMEM_ST16(tS + c, s);
-          }
-          tmem_wait_st();
-        }
         float p[kKeys];
         {
           uint32_t* u = reinterpret_cast<uint32_t*>(p);
@@ -663,6 +680,20 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < kKeys; ++k) asm volatile("" : "+f"(p[k]));
+        }
+        if (tile >= special) {
+          const int64_t left = (int64_t)vis - (int64_t)tile * kKeys;
+          const int seen = (int)(left < 0 ? 0 : left > kKeys ? kKeys : left);
+          if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // (by bits of a word: one instruction sets seven predicates)
+              const int in = seen - 32 * c;
+              const uint32_t bits = in >= 32 ? 0xffffffffu : in <= 0 ? 0u : (1u << in) - 1u;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(bits >> k & 1u)) p[32 * c + k] = -INFINITY;
+            }
+          }
         }
         float top;  // NaN if a score is, so that the row becomes NaN
         {
@@ -683,7 +714,8 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           l.x *= keep;
           l.y *= keep;
           if (j > 0) {
-            if (!wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) {
+            // (with two lanes these scores were issued after the product before, so that it is over)
+            if (ONE && !wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -743,7 +775,8 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         ++tile_uses;
       }
       // the last product of this lane, then O / l
-      if (ok && n > 0) ok = wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag);
+      if (ok && n > 0) ok = wait_warp(bar(L::o + r), (ONE ? tile_uses - 1 : units_done) & 1, abort_flag);
+      units_done += n > 0;
       const int64_t rh = (int64_t)(x.s.q0 + (at >> a.pack_log)) * a.H + x.h + (at & (a.pack - 1));
       const int64_t part = (int64_t)x.part * a.rows_per_unit + r * kRows + row;
       float* const lse_at = x.part >= 0 ? a.part_lse + part : a.lse + rh;
