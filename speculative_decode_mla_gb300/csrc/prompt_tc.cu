@@ -443,10 +443,12 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         };
         for (int j = 0; j < n && ok; ++j) {
           const int at = x.s.k0 + (x.t0 + j) * kKeys, keys = L::keys + (tiles & 3), vals = L::vals + (tiles & 3);
+          if (!ONE && j == 0) ok = load_q(0);  // (free before the ring's blocks are)
+          if (!ok) break;
           mbar_arrive_expect_tx(bar(keys), 3 * kBlock);
           ok = load_block(&map_k, 0, x.g, at, keys, false) && load_block(&map_k, 64, x.g, at, keys, false) &&
                load_block(&map_kr, 0, 0, at, keys, false);
-          if (ok && j == 0) ok = load_q(0) && (ONE || load_q(1));
+          if (ok && j == 0) ok = load_q(ONE ? 0 : 1);
           if (!ok) break;
           mbar_arrive_expect_tx(bar(vals), 2 * kBlock);
           ok = load_block(&map_v, 0, x.g, at, vals, true) && load_block(&map_v, 0, x.g, at + 64, vals, true);
@@ -585,7 +587,9 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
 #pragma unroll 1
           for (int j = -1; j < n && ok; ++j) {
             const uint32_t here = tiles + j;
-#pragma unroll
+            // (one body for both lanes: at 83 to 93% hits the instruction cache is what every unit's beginning and end wait for. 24
+            // sequences of 61 to 2048 rows: 113 us, with a body for each lane 117)
+#pragma unroll 1
             for (int r = 0; r < 2; ++r) {
               const int of_lane = r ? n1 : n0;
               if (ok && j >= 0 && j < of_lane) ok = values(r, r, here, j == 0, j + 1 == of_lane);
@@ -646,7 +650,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           const auto piece = [&](int c) { return values + (c >> 3) * (kBlock / 32) + ((c + row) & 7); };
           const bool behind = (int64_t)tile * kKeys + row >= x.s.n;
           uint32_t top = 0;  // bits 15 and 31: some exponent is all ones
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < 16; ++c) {
             const uint4 d = *piece(c);
             top |= ((d.x & 0x7f807f80u) + 0x00800080u) | ((d.y & 0x7f807f80u) + 0x00800080u) | ((d.z & 0x7f807f80u) + 0x00800080u) |
