@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
   const uint32_t tmem = *tmem_slot;
   // everything above read no global memory
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.shared) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge, which waits for this kernel's end
 
   const auto fewer_registers = [&] {
     if (!ONE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::other_regs));
@@ -918,6 +919,7 @@ __device__ __forceinline__ T block_scan(T v, T* sums, T& all) {
 __global__ void __launch_bounds__(kListThreads) prompt_list_kernel(const PromptArgs a) {
   __shared__ int32_t bins[kBins];
   __shared__ int32_t sums[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention, which sets itself up and waits for this kernel's end
   const int64_t most = ((int64_t)a.max_k + kKeys - 1) / kKeys;
   int shift = 0;
   while ((most >> shift) >= kBins) ++shift;
@@ -943,6 +945,7 @@ static_assert(kBins == 2 * kListThreads, "two bins a thread");
 __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const PromptArgs a) {
   __shared__ int32_t sums[32];
   __shared__ int32_t work;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int heads = a.virtual_heads;
   if (threadIdx.x == 0) work = 0;
   __syncthreads();
