@@ -139,10 +139,12 @@ int mla_prompt_workspace_size(const mla_prompt_desc *desc, size_t *bytes);
  *   cu_q, cu_k  device int32 [B + 1], not falling, within [0, num_q] and [0, num_k]; cu_k may be cu_q itself. Values outside, and
  *            lengths outside [0, max_q_len] or [0, max_k_len], are clamped (MLA_CHECK_BAD_LENGTH under debug checks).
  *   out      device [num_q][H][128], bf16 or float32, 16-byte aligned;  lse  device float32 [num_q][H].
- *   workspace  device, >= mla_prompt_workspace_size bytes, 256-byte aligned (NULL where that is 0).
+ *   workspace  device, >= mla_prompt_workspace_size bytes, 256-byte aligned (NULL where that is 0). Nothing is kept in it: calls
+ *            that run one after the other may share it, captured ones too; calls that run at once may not.
  *   dev_status as for mla_verify_attn.
  * Weights are rounded to bf16 for the product with V; scores, maxima, sums and outputs are float32, and
- * where a row's keys are cut into parts (calls with few units, by the lengths on the device) these are merged in float32. out, lse and workspace may overlap nothing else of the call.
+ * where a row's keys are cut into parts (calls with few units, by the lengths on the device) these are merged in float32. out, lse and
+ * workspace may overlap nothing else of the call.
  */
 int mla_prompt_attn(const mla_prompt_desc *desc, const void *q, const void *k_nope, const void *k_rope, const void *v,
                     const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse, void *workspace,
