@@ -68,12 +68,13 @@ __device__ __forceinline__ void clamp_range(const PromptArgs& a, int32_t lo, int
   at = (int32_t)l;
   len = (int32_t)(h - l);
 }
-__device__ __forceinline__ PromptSeq load_seq(const PromptArgs& a, int b) {
+__device__ __forceinline__ PromptSeq clamp_seq(const PromptArgs& a, int32_t q0, int32_t q1, int32_t k0, int32_t k1) {
   PromptSeq s;
-  clamp_range(a, a.cu_q[b], a.cu_q[b + 1], a.num_q, a.max_q, s.q0, s.m);
-  clamp_range(a, a.cu_k[b], a.cu_k[b + 1], a.num_k, a.max_k, s.k0, s.n);
+  clamp_range(a, q0, q1, a.num_q, a.max_q, s.q0, s.m);
+  clamp_range(a, k0, k1, a.num_k, a.max_k, s.k0, s.n);
   return s;
 }
+__device__ __forceinline__ PromptSeq load_seq(const PromptArgs& a, int b) { return clamp_seq(a, a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1]); }
 // How many keys query i of a sequence sees (the first so many).
 __device__ __forceinline__ int32_t visible(const PromptArgs& a, const PromptSeq& s, int32_t i) {
   return a.causal ? max(0, i - s.m + 1 + s.n) : s.n;  // (i < m)
@@ -93,6 +94,10 @@ __device__ __forceinline__ int sequence_of(const PromptArgs& a, int64_t row, Pro
 // Tiles of keys that a unit's rows [row0, row1) of a sequence see.
 __device__ __forceinline__ int32_t tiles_of(const PromptArgs& a, const PromptSeq& s, int64_t row1) {
   return (int32_t)(((int64_t)visible(a, s, (int32_t)((row1 - 1) >> a.pack_log)) + kPromptTile - 1) / kPromptTile);
+}
+// Units that so many rows make (of 128 or 256 rows).
+__device__ __forceinline__ int32_t units_in(const PromptArgs& a, int64_t rows) {
+  return (int32_t)((rows + a.rows_per_unit - 1) >> (a.rows_per_unit > kPromptTile ? 8 : 7));
 }
 // Units of work of an entry and virtual head: its tiles, at least one, and what a run costs besides.
 __device__ __forceinline__ int32_t cost_of(int32_t tiles) { return max(1, tiles) + kUnitCost; }

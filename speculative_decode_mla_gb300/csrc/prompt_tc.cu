@@ -180,17 +180,15 @@ struct Unit {
 };
 static_assert(sizeof(Unit) <= kUnitWords * 4, "unit description");
 
-// Row tile `tile` of sequence b (-1: none), heads of virtual head vh, all tiles.
-__device__ __forceinline__ Unit unit_of(const PromptArgs& a, int b, int tile, int vh) {
+// Row tile `tile` of sequence s, heads of virtual head vh, all tiles.
+__device__ __forceinline__ Unit unit_of(const PromptArgs& a, const PromptSeq& s, int tile, int vh) {
   Unit x;
   x.live = 1;
   x.part = -1;
   x.h = vh * a.pack;
   x.g = x.h / a.group;
   x.t0 = x.special = x.tiles[0] = x.tiles[1] = x.row0 = x.rows = x.all = 0;
-  x.s.q0 = x.s.m = x.s.k0 = x.s.n = 0;
-  if (b < 0) return x;
-  x.s = load_seq(a, b);
+  x.s = s;
   const int64_t rows = (int64_t)x.s.m << a.pack_log, row0 = (int64_t)tile * a.rows_per_unit;
   if (row0 >= rows) return x;
   x.row0 = (int32_t)row0;
@@ -206,19 +204,37 @@ __device__ __forceinline__ void cut(const PromptArgs& a, Unit& x, int32_t t0, in
   x.tiles[0] = x.all ? max(0, min(t1, tiles_of(a, x.s, min((int64_t)x.rows, mid))) - t0) : 0;
   x.tiles[1] = a.rows_per_unit > kRows && x.rows > mid ? t1 - t0 : 0;
 }
-// Unit number u of a call that is not shared (virtual heads in groups of a.head_group; in a group by row tile, then head).
-__device__ __forceinline__ Unit unit_at(const PromptArgs& a, uint32_t u) {
+// Unit number u of a call that is not shared (virtual heads in groups of a.head_group; in a group by row tile, then head), found in
+// steps whose reads of memory wait for each other: a step's results are used by the next one, some tiles later.
+struct Place {
+  int b, tile, vh;          // sequence (-1: none)
+  int32_t q0, q1, k0, k1;   // its ends, as they are in memory
+};
+__device__ __forceinline__ Place place_of(const PromptArgs& a, uint32_t u) {
   const uint32_t full = (uint32_t)a.entries * (uint32_t)a.head_group, group = u / full;  // (all units together are below 2^31)
   const uint32_t heads = min(a.head_group, a.virtual_heads - (int)group * a.head_group);
   const uint32_t rest = u - group * full, e = rest / heads;
-  const int vh = (int)(group * a.head_group + (rest - e * heads));
-  int b = 0, tile = (int)((uint32_t)a.entries - 1 - e);
+  Place at = {};
+  at.vh = (int)(group * a.head_group + (rest - e * heads));
+  at.tile = (int)((uint32_t)a.entries - 1 - e);
   if (a.listed) {
-    const int2 at = a.list[e];
-    b = at.x;
-    tile = at.y;
+    const int2 entry = a.list[e];
+    at.b = entry.x;
+    at.tile = entry.y;
   }
-  Unit x = unit_of(a, b, tile, vh);
+  return at;
+}
+__device__ __forceinline__ void read_ends(const PromptArgs& a, Place& at) {
+  if (at.b < 0) return;
+  at.q0 = a.cu_q[at.b];
+  at.q1 = a.cu_q[at.b + 1];
+  at.k0 = a.cu_k[at.b];
+  at.k1 = a.cu_k[at.b + 1];
+}
+__device__ __forceinline__ Unit unit_at(const PromptArgs& a, const Place& at) {
+  PromptSeq s = {0, 0, 0, 0};
+  if (at.b >= 0) s = clamp_seq(a, at.q0, at.q1, at.k0, at.k1);
+  Unit x = unit_of(a, s, at.tile, at.vh);
   cut(a, x, 0, x.all);
   return x;
 }
@@ -249,9 +265,10 @@ __device__ __forceinline__ Walk walk_from(const PromptArgs& a, int c, int lane) 
     return k;
   }
   const PromptSeq s = load_seq(a, 0);
-  const int32_t rows = s.m << a.pack_log, n = (rows + a.rows_per_unit - 1) / a.rows_per_unit;
+  const int32_t rows = s.m << a.pack_log, n = units_in(a, rows);
   const auto cost = [&](int32_t e) { return e < n ? cost_of(tiles_of(a, s, min(rows, (e + 1) * a.rows_per_unit))) * a.virtual_heads : 0; };
   int32_t total = 0;
+#pragma unroll 1
   for (int32_t e = lane; e < n; e += 32) total += cost(e);
   total = __reduce_add_sync(0xffffffffu, total);
   k.share = share_of(a, total);
@@ -259,6 +276,7 @@ __device__ __forceinline__ Walk walk_from(const PromptArgs& a, int c, int lane) 
   k.w_end = k.w + min(k.share, total - k.w);
   k.entry = -1;
   int32_t before = 0;
+#pragma unroll 1
   for (int32_t e0 = 0; e0 < n && k.w < k.w_end; e0 += 32) {
     const int32_t own = cost(e0 + lane);
     int32_t inc = own;
@@ -285,6 +303,7 @@ __device__ __forceinline__ Walk walk_from(const PromptArgs& a, int c, int lane) 
 __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, PromptMerge* merge) {
   Unit x;
   x.live = 0;
+#pragma unroll 1
   while (k.w < k.w_end) {
     int b = 0, tile = k.entry;
     if (a.listed) {
@@ -292,7 +311,7 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
       b = at.x;
       tile = at.y;
     }
-    x = unit_of(a, b, tile, k.head);
+    x = unit_of(a, load_seq(a, b), tile, k.head);
     const int32_t len = max(1, x.all), off = k.offset, take = min(len - off, k.w_end - k.w);
     if (off < len) {
       cut(a, x, off, min(x.all, off + take));
@@ -401,8 +420,12 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       };
       bool next_asked = false;
       uint32_t n_unit = 0, n_asked = 0;
-      int64_t u = blockIdx.x;
-      bool ok = true;
+      bool ok = true, more = true;  // more: there is a next unit, at `place`
+      Place place = {};
+      if (!a.shared) {
+        place = place_of(a, blockIdx.x);
+        read_ends(a, place);
+      }
       PromptMerge merge = {};
       while (ok) {
         const int slot = n_unit & 1;
@@ -412,8 +435,8 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         if (a.shared) {
           x = next_part(a, walk, blockIdx.x, &merge);
           if (n_unit == 0) a.merges[blockIdx.x] = merge;
-        } else if (u >= 0) {
-          x = unit_at(a, (uint32_t)u);
+        } else if (more) {
+          x = unit_at(a, place);
         }
         // (a unit without rows, where the lengths leave fewer than the call has room for, is passed over)
         const bool none = !a.shared && x.live && x.rows == 0;
@@ -442,34 +465,40 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           ++q_loads[r];
           return true;
         };
-        for (int j = 0; j < n && ok; ++j) {
-          const int at = x.s.k0 + (x.t0 + j) * kKeys, keys = L::keys + (tiles & 3), vals = L::vals + (tiles & 3);
-          if (!ONE && j == 0) ok = load_q(0);  // (free before the ring's blocks are)
-          if (!ok) break;
-          mbar_arrive_expect_tx(bar(keys), 3 * kBlock);
-          ok = load_block(&map_k, 0, x.g, at, keys, false) && load_block(&map_k, 64, x.g, at, keys, false) &&
-               load_block(&map_kr, 0, 0, at, keys, false);
-          if (ok && j == 0) ok = load_q(ONE ? 0 : 1);
-          if (!ok) break;
-          mbar_arrive_expect_tx(bar(vals), 2 * kBlock);
-          ok = load_block(&map_v, 0, x.g, at, vals, true) && load_block(&map_v, 0, x.g, at + 64, vals, true);
-          ++tiles;
-        }
-        if (ok && !a.shared) {
-          ok = wait_bar(bar(L::next), n_asked & 1, abort_flag);
-          if (!ok) break;
-          ++n_asked;
-          next_asked = false;
-          uint32_t got, id;
-          asm volatile(
-              "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b64 lo, hi;\n"
-              "ld.shared.v2.b64 {lo, hi}, [%2];\nmov.b128 h, {lo, hi};\n"
-              "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
-              "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
-              : "=r"(got), "=r"(id)
-              : "r"(base + L::answer)
-              : "memory");
-          u = got ? (int64_t)id : -1;
+        for (int j = 0; j < max(n, 2) && ok; ++j) {
+          if (j < n) {
+            const int at = x.s.k0 + (x.t0 + j) * kKeys, keys = L::keys + (tiles & 3), vals = L::vals + (tiles & 3);
+            if (!ONE && j == 0) ok = load_q(0);  // (free before the ring's blocks are)
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar(keys), 3 * kBlock);
+            ok = load_block(&map_k, 0, x.g, at, keys, false) && load_block(&map_k, 64, x.g, at, keys, false) &&
+                 load_block(&map_kr, 0, 0, at, keys, false);
+            if (ok && j == 0) ok = load_q(ONE ? 0 : 1);
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar(vals), 2 * kBlock);
+            ok = load_block(&map_v, 0, x.g, at, vals, true) && load_block(&map_v, 0, x.g, at + 64, vals, true);
+            ++tiles;
+          }
+          if (a.shared || !ok) continue;
+          if (j == 0) {
+            ok = wait_bar(bar(L::next), n_asked & 1, abort_flag);
+            if (!ok) break;
+            ++n_asked;
+            next_asked = false;
+            uint32_t got, id;
+            asm volatile(
+                "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b64 lo, hi;\n"
+                "ld.shared.v2.b64 {lo, hi}, [%2];\nmov.b128 h, {lo, hi};\n"
+                "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+                "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
+                : "=r"(got), "=r"(id)
+                : "r"(base + L::answer)
+                : "memory");
+            more = got != 0;
+            if (more) place = place_of(a, id);
+          } else if (j == 1 && more) {
+            read_ends(a, place);
+          }
         }
         if (!none) ++n_unit;
       }
@@ -829,7 +858,11 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       const int specials = max(0, t0 + n - max(t0, special));
       const uint32_t* const odd_at = bad + (slot * kMaxSpecial + max(t0 - special, 0)) * 4;
       uint32_t odd = 0;
-      for (int k = 0; k < specials * 4; ++k) odd |= odd_at[k];
+#pragma unroll 1
+      for (int k = 0; k < specials; ++k) {
+        const uint4 of_tile = reinterpret_cast<const uint4*>(odd_at)[k];
+        odd |= of_tile.x | of_tile.y | of_tile.z | of_tile.w;
+      }
       if (odd && real) {
 #pragma unroll 1
         for (int t = 0; t < specials * kKeys; ++t) {
@@ -869,13 +902,16 @@ constexpr int kAlone = 4;  // a thread deals with a sequence of so many row tile
 template <class Use>
 __device__ __forceinline__ void each_entry(const PromptArgs& a, Use use) {
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
   for (int b0 = threadIdx.x - lane; b0 < a.B; b0 += kListThreads) {
     PromptSeq s = {0, 0, 0, 0};
     if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
     const int64_t rows = (int64_t)s.m << a.pack_log;
-    const int32_t n = (int32_t)((rows + a.rows_per_unit - 1) / a.rows_per_unit);
+    const int32_t n = units_in(a, rows);
     if (n <= kAlone)
+#pragma unroll 1
       for (int32_t t = 0; t < n; ++t) use(b0 + lane, t, tiles_of(a, s, min(rows, ((int64_t)t + 1) * a.rows_per_unit)));
+#pragma unroll 1
     for (uint32_t left = __ballot_sync(0xffffffffu, n > kAlone); left; left &= left - 1) {
       const int l = __ffs(left) - 1;
       PromptSeq o;
@@ -883,7 +919,8 @@ __device__ __forceinline__ void each_entry(const PromptArgs& a, Use use) {
       o.m = __shfl_sync(0xffffffffu, s.m, l);
       o.n = __shfl_sync(0xffffffffu, s.n, l);
       const int64_t o_rows = (int64_t)o.m << a.pack_log;
-      const int32_t o_n = (int32_t)((o_rows + a.rows_per_unit - 1) / a.rows_per_unit);
+      const int32_t o_n = units_in(a, o_rows);
+#pragma unroll 1
       for (int32_t t = lane; t < o_n; t += 32) use(b0 + l, t, tiles_of(a, o, min(o_rows, ((int64_t)t + 1) * a.rows_per_unit)));
     }
   }
@@ -923,6 +960,7 @@ __global__ void __launch_bounds__(kListThreads) prompt_list_kernel(const PromptA
   const int64_t most = ((int64_t)a.max_k + kKeys - 1) / kKeys;
   int shift = 0;
   while ((most >> shift) >= kBins) ++shift;
+#pragma unroll 1
   for (int i = threadIdx.x; i < kBins; i += kListThreads) bins[i] = 0;
   __syncthreads();
   each_entry(a, [&](int, int, int32_t tiles) { atomicAdd(&bins[kBins - 1 - (tiles >> shift)], 1); });
@@ -937,6 +975,7 @@ __global__ void __launch_bounds__(kListThreads) prompt_list_kernel(const PromptA
     const int32_t at = atomicAdd(&bins[kBins - 1 - (tiles >> shift)], 1);
     if (at < a.entries) a.list[at] = make_int2(b, t);
   });
+#pragma unroll 1
   for (int64_t i = all + threadIdx.x; i < a.entries; i += kListThreads) a.list[i] = make_int2(-1, 0);
 }
 static_assert(kBins == 2 * kListThreads, "two bins a thread");
@@ -959,6 +998,7 @@ __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const Prompt
     a.starts[a.ctas].offset = share;
     a.starts[a.ctas + 1].offset = total;
   }
+#pragma unroll 1
   for (int32_t c = threadIdx.x; c < a.ctas; c += kListThreads)
     if ((int64_t)c * share >= total) a.starts[c].entry = -1;
   // sequences in blocks of kListThreads: the entries and the work before a thread's sequence, then its own entries
@@ -966,6 +1006,7 @@ __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const Prompt
   const auto write = [&](int b, int t, int32_t e, int32_t w, int32_t cost) {
     const int32_t lo = w * heads, hi = lo + cost * heads;
     if (e < a.entries) a.list[e] = make_int2(b, t);
+#pragma unroll 1
     for (int32_t c = lo / share + (lo % share ? 1 : 0); c < a.ctas && (int64_t)c * share < hi; ++c) {
       a.starts[c].entry = e;
       a.starts[c].head = (c * share - lo) / cost;
@@ -973,11 +1014,12 @@ __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const Prompt
     }
   };
   int32_t entry0 = 0, work0 = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.B; b0 += kListThreads) {
     const int b = b0 + threadIdx.x;
     PromptSeq s = {0, 0, 0, 0};
     if (b < a.B) s = load_seq(a, b);
-    const int32_t n = ((s.m << a.pack_log) + a.rows_per_unit - 1) / a.rows_per_unit;
+    const int32_t n = units_in(a, s.m << a.pack_log);
     const auto cost = [&](const PromptSeq& o, int32_t t) {
       return cost_of(tiles_of(a, o, min(o.m << a.pack_log, (t + 1) * a.rows_per_unit)));
     };
@@ -990,12 +1032,15 @@ __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const Prompt
     const uint32_t longer = __ballot_sync(0xffffffffu, n > kAlone);
     int32_t own = 0, entries, works;
     if (n <= kAlone)
+#pragma unroll 1
       for (int32_t t = 0; t < n; ++t) own += cost(s, t);
+#pragma unroll 1
     for (uint32_t left = longer; left; left &= left - 1) {
       const int l = __ffs(left) - 1;
       const PromptSeq o = of_lane(l);
       const int32_t o_n = __shfl_sync(0xffffffffu, n, l);
       int32_t sum = 0;
+#pragma unroll 1
       for (int32_t t = lane; t < o_n; t += 32) sum += cost(o, t);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -1004,16 +1049,19 @@ __global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const Prompt
     const int32_t e = entry0 + block_scan(n, sums, entries);
     int32_t w = work0 + block_scan(own, sums, works);
     if (n <= kAlone)
+#pragma unroll 1
       for (int32_t t = 0; t < n; ++t) {
         const int32_t c = cost(s, t);
         write(b, t, e + t, w, c);
         w += c;
       }
+#pragma unroll 1
     for (uint32_t left = longer; left; left &= left - 1) {
       const int l = __ffs(left) - 1;
       const PromptSeq o = of_lane(l);
       const int32_t o_n = __shfl_sync(0xffffffffu, n, l), o_e = __shfl_sync(0xffffffffu, e, l);
       int32_t o_w = __shfl_sync(0xffffffffu, w, l);
+#pragma unroll 1
       for (int32_t t0 = 0; t0 < o_n; t0 += 32) {
         const int32_t c = t0 + lane < o_n ? cost(o, t0 + lane) : 0;
         int32_t inc = c;
