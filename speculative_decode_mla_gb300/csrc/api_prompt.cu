@@ -40,9 +40,10 @@ int32_t pack_of(const mla_prompt_desc& d) {
   return group <= kPromptTile && (group & (group - 1)) == 0 ? group : 1;
 }
 int64_t longest_q(const mla_prompt_desc& d) { return d.max_q_len < d.num_q ? d.max_q_len : d.num_q; }
-// Row tiles of all sequences, at most.
+// Row tiles of all sequences, at most: whatever the ends in memory are, and where they do not fall.
+int64_t any_entries(const mla_prompt_desc& d, int64_t rows) { return d.num_seqs * cdiv(longest_q(d) * pack_of(d), rows); }
 int64_t entries_of(const mla_prompt_desc& d, int64_t rows) {
-  const int64_t pack = pack_of(d), a = d.num_seqs * cdiv(longest_q(d) * pack, rows), b = d.num_q * pack / rows + d.num_seqs;
+  const int64_t a = any_entries(d, rows), b = d.num_q * pack_of(d) / rows + d.num_seqs;
   return a < b ? a : b;
 }
 int64_t pad(int64_t bytes) { return cdiv(bytes, 256) * 256; }
@@ -67,9 +68,10 @@ extern "C" int mla_prompt_plan(const mla_prompt_desc* d, int32_t num_sms, mla_pr
   } else {
     p.rows_per_unit = longest_q(*d) * p.pack <= kPromptTile ? kPromptTile : kMaxUnitRows;
     p.listed = d->num_seqs > 1;
-    const int64_t units = entries_of(*d, p.rows_per_unit) * (d->num_heads / p.pack);
+    const int64_t heads = d->num_heads / p.pack, units = entries_of(*d, p.rows_per_unit) * heads;
     // (the kernels count the work of shared calls in 32 bits)
-    const bool fits = units * (tiles + 1 + kUnitCost) < 0x40000000;
+    const int64_t most = any_entries(*d, p.rows_per_unit);
+    const bool fits = most < 0x40000000 && most * heads < 0x40000000 && most * heads * (tiles + 1 + kUnitCost) < 0x40000000;
     if (d->num_ctas > 0 && !fits) return MLA_ERR_UNSUPPORTED;
     p.shared = units > 0 && fits && (d->num_ctas > 0 || (units < kSharedUnits * num_sms && tiles > kLeastShare));
     p.ctas = !p.shared ? units : d->num_ctas > 0 ? d->num_ctas : num_sms;

@@ -311,7 +311,7 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
   Unit x;
   x.live = 0;
 #pragma unroll 1
-  while (k.w < k.w_end) {
+  while (k.w < k.w_end && k.entry < a.entries) {  // (ends that fall, against the contract, can give more entries than there is room for)
     int b = 0, tile = k.entry;
     if (a.listed) {
       const int2 at = a.list[k.entry];

@@ -130,3 +130,19 @@ def test_rows_out_and_heads_in_place_over_their_inputs():
     r, h = rows.clone(), q.clone()
     lib.rope_append(None, r, None, pos, table, weight=w, q=h, q_weight=qw, halves=True, rows_out=r, q_out=h)
     assert same((r, h), want)
+
+
+@pytest.mark.parametrize("ctas", [0, 3, 152])
+def test_ends_that_fall_are_reported_and_stay_in_bounds(ctas):
+    """Ends that fall again and again give more units than the rows of q can make: what there is no room for is left out."""
+    import torch
+    import speculative_decode_mla_gb300 as lib
+    p = problem([1000], [1000], 2, seed=7)
+    want = lib.prompt_attn(**p, num_ctas=ctas)
+    bad = {**p, "cu_q": ints([0, 1000] * 5), "cu_k": ints([0, 1000] * 5)}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib.prompt_attn(**bad, num_ctas=ctas)
+    with pytest.raises(lib.MLAError):
+        lib.prompt_attn(**bad, num_ctas=ctas, flags=lib.MLA_FLAG_DEBUG_CHECKS, dev_status=status)
+    assert int(status) == lib.CHECK_BAD_LENGTH
+    assert same(lib.prompt_attn(**p, num_ctas=ctas), want)
