@@ -110,7 +110,7 @@ typedef struct mla_prompt_plan_t {
   int32_t rows_per_unit;   /* rows (query and head) that a CTA works on at a time: 256, or 128 when no sequence has more */
   int32_t pack;            /* query heads of one key head that share a unit's rows: H / num_kv_heads, or 1 */
   int32_t shared;          /* 1: the CTAs share all tiles of keys evenly, and parts of a unit are merged; 0: whole units */
-  int32_t listed;          /* 1: a first kernel lists the batch's units */
+  int32_t listed;          /* 1: a first kernel lists the units of a batch, longest first (with shared 0) */
   int32_t reserved;
   int64_t ctas;            /* CTAs launched: with shared 0, an upper bound of the units */
   int64_t workspace_bytes; /* 0 when none is needed */

@@ -67,18 +67,18 @@ extern "C" int mla_prompt_plan(const mla_prompt_desc* d, int32_t num_sms, mla_pr
     p.ctas = d->num_q * d->num_heads;
   } else {
     p.rows_per_unit = longest_q(*d) * p.pack <= kPromptTile ? kPromptTile : kMaxUnitRows;
-    p.listed = d->num_seqs > 1;
     const int64_t heads = d->num_heads / p.pack, units = entries_of(*d, p.rows_per_unit) * heads;
     // (the kernels count the work of shared calls in 32 bits)
     const int64_t most = any_entries(*d, p.rows_per_unit);
     const bool fits = most < 0x40000000 && most * heads < 0x40000000 && most * heads * (tiles + 1 + kUnitCost) < 0x40000000;
     if (d->num_ctas > 0 && !fits) return MLA_ERR_UNSUPPORTED;
     p.shared = units > 0 && fits && (d->num_ctas > 0 || (units < kSharedUnits * num_sms && tiles > kLeastShare));
+    p.listed = d->num_seqs > 1 && !p.shared;
     p.ctas = !p.shared ? units : d->num_ctas > 0 ? d->num_ctas : num_sms;
     if (p.shared && p.ctas > kMaxPromptCtas) p.ctas = kMaxPromptCtas;
     if (p.shared)
       p.workspace_bytes = pad(p.ctas * 2 * p.rows_per_unit * kHeadV * 4) + pad(p.ctas * 2 * p.rows_per_unit * 4) +
-                          pad(p.ctas * (int64_t)sizeof(PromptMerge)) + (p.listed ? pad((p.ctas + 2) * (int64_t)sizeof(PromptStart)) : 0);
+                          pad(p.ctas * (int64_t)sizeof(PromptMerge));
     if (p.listed) p.workspace_bytes += pad(entries_of(*d, p.rows_per_unit) * (int64_t)sizeof(int2));
   }
   if (p.ctas > 0x7fffffff) return MLA_ERR_UNSUPPORTED;
@@ -141,7 +141,6 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
     a.part_o = reinterpret_cast<float*>(take(p.ctas * 2 * p.rows_per_unit * kHeadV * 4));
     a.part_lse = reinterpret_cast<float*>(take(p.ctas * 2 * p.rows_per_unit * 4));
     a.merges = reinterpret_cast<PromptMerge*>(take(p.ctas * (int64_t)sizeof(PromptMerge)));
-    if (p.listed) a.starts = reinterpret_cast<PromptStart*>(take((p.ctas + 2) * (int64_t)sizeof(PromptStart)));
   }
   a.list = reinterpret_cast<int2*>(ws);
   a.dev_status = dev_status;

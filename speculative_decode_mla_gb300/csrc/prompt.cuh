@@ -15,10 +15,6 @@ constexpr int kMaxUnitRows = 2 * kPromptTile;
 // What starting and ending a run of tiles costs, in tiles, and the least that a CTA takes in shared calls.
 constexpr int kUnitCost = 2, kLeastShare = 4;
 
-// Where a CTA of a shared call begins: its first entry, virtual head and tile there, or entry -1.
-struct PromptStart {
-  int32_t entry, head, offset, reserved;
-};
 // A unit whose last part CTA number c computed, with the first one's CTA: parts first .. c, to be merged.
 struct PromptMerge {
   int32_t live, first, slot;  // slot of the first part (the others have slot 0)
@@ -39,8 +35,7 @@ struct PromptArgs {
   float* part_o;      // shared: [ctas][2][rows_per_unit][128], parts of units, each normalised over its own keys
   float* part_lse;    // [ctas][2][rows_per_unit]
   PromptMerge* merges;  // [ctas]
-  PromptStart* starts;  // shared and listed: [ctas]
-  int2* list;         // listed: (sequence, row tile) of every entry, longest first (shared: in order), then (-1, 0)
+  int2* list;         // listed: (sequence, row tile) of every entry, longest first, then (-1, 0)
   int32_t* dev_status;
   int64_t num_q, num_k;
   int64_t q_ts, q_hs, k_ts, k_hs, kr_ts, v_ts, v_hs;

@@ -45,6 +45,7 @@ constexpr int kTileBlocks = 5;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 constexpr int kMaxSpecial = 3;                // tiles that some row of a unit does not see whole, and another does in part
 constexpr int kUnitWords = 24;
+constexpr int kAlone = 4;                     // a thread deals with a sequence of so many row tiles alone, a warp with a longer one
 
 template <bool ONE>
 struct Layout {
@@ -250,58 +251,103 @@ __device__ __forceinline__ Unit unit_at(const PromptArgs& a, const Place& at) {
 __device__ __forceinline__ int32_t share_of(const PromptArgs& a, int32_t total) {
   return max(kLeastShare + kUnitCost, total / a.ctas + (total % a.ctas ? 1 : 0));
 }
-// A CTA's way through its share of a shared call: entries in order, the virtual heads of an entry one after the other, each
-// cost_of(its tiles) units of work, of which the last kUnitCost stand for starting and ending it.
+// Cost of row tile t of a sequence, for one virtual head.
+__device__ __forceinline__ int32_t entry_cost(const PromptArgs& a, const PromptSeq& s, int32_t t) {
+  return cost_of(tiles_of(a, s, min((int64_t)s.m << a.pack_log, ((int64_t)t + 1) * a.rows_per_unit)));
+}
+// Cost of all n row tiles of a lane's sequence; every lane of the warp calls it. A lane deals with a short sequence alone, the warp with a
+// longer one.
+__device__ __forceinline__ int32_t sequence_cost(const PromptArgs& a, const PromptSeq& s, int32_t n, int lane) {
+  int32_t own = 0;
+  if (n <= kAlone)
+#pragma unroll 1
+    for (int32_t t = 0; t < n; ++t) own += entry_cost(a, s, t);
+#pragma unroll 1
+  for (uint32_t left = __ballot_sync(0xffffffffu, n > kAlone); left; left &= left - 1) {
+    const int l = __ffs(left) - 1;
+    PromptSeq o = {0, 0, 0, 0};
+    o.m = __shfl_sync(0xffffffffu, s.m, l);
+    o.n = __shfl_sync(0xffffffffu, s.n, l);
+    const int32_t o_n = __shfl_sync(0xffffffffu, n, l);
+    int32_t sum = 0;
+#pragma unroll 1
+    for (int32_t t = lane; t < o_n; t += 32) sum += entry_cost(a, o, t);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == l) own = sum;
+  }
+  return own;
+}
+// Where in the lanes' work (own each, `before` before them) place w lies: the lane, or -1; what lies before that lane is left in `before`.
+__device__ __forceinline__ int lane_at(int32_t own, int32_t w, int32_t& before, int lane) {
+  int32_t inc = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t up = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += up;
+  }
+  const uint32_t past = __ballot_sync(0xffffffffu, before + inc > w);
+  const int l = past ? __ffs(past) - 1 : 31;
+  before += __shfl_sync(0xffffffffu, past ? inc - own : inc, l);
+  return past ? l : -1;
+}
+// A CTA's way through its share of a shared call: sequences in order, their row tiles in order, the virtual heads of a row tile one
+// after the other, each cost_of(its tiles) units of work, of which the last kUnitCost stand for starting and ending it.
 struct Walk {
   int32_t w, w_end, offset, share;  // offset: of w in the unit (all work together is below 2^31: mla_prompt_plan)
-  int32_t entry, head;
+  int32_t b, tile, num_tiles, head;
+  PromptSeq s;
   bool first;
 };
-// Where share number c begins (every lane of the warp calls it).
+// Where share number c begins (every lane of the warp calls it). Every CTA goes through all sequences for itself: such calls have few
+// units. (61 single tokens: 58.2 us, 59.6 and one launch more with a kernel before this one that shares out; one sequence alone loses 0.3 us.)
 __device__ __forceinline__ Walk walk_from(const PromptArgs& a, int c, int lane) {
-  Walk k;
+  Walk k = {};
   k.first = true;
-  if (a.listed) {
-    const PromptStart s = a.starts[c];
-    k.entry = s.entry;
-    k.head = s.head;
-    k.offset = s.offset;
-    k.share = a.starts[a.ctas].offset;
-    k.w = s.entry < 0 ? 0 : c * k.share;
-    k.w_end = s.entry < 0 ? 0 : k.w + min(k.share, a.starts[a.ctas + 1].offset - k.w);
-    return k;
-  }
-  const PromptSeq s = load_seq(a, 0);
-  const int32_t rows = s.m << a.pack_log, n = units_in(a, rows);
-  const auto cost = [&](int32_t e) { return e < n ? cost_of(tiles_of(a, s, min(rows, (e + 1) * a.rows_per_unit))) * a.virtual_heads : 0; };
-  int32_t total = 0;
+  k.b = a.B;
+  PromptSeq s = {0, 0, 0, 0};
+  int32_t n = 0, own = 0, total = 0, before = 0;
 #pragma unroll 1
-  for (int32_t e = lane; e < n; e += 32) total += cost(e);
-  total = __reduce_add_sync(0xffffffffu, total);
-  k.share = share_of(a, total);
-  k.w = (int32_t)min((int64_t)total, (int64_t)c * k.share);
-  k.w_end = k.w + min(k.share, total - k.w);
-  k.entry = -1;
-  int32_t before = 0;
+  for (int pass = 0; pass < 2; ++pass) {  // all work; then the sequence where the share begins
 #pragma unroll 1
-  for (int32_t e0 = 0; e0 < n && k.w < k.w_end; e0 += 32) {
-    const int32_t own = cost(e0 + lane);
-    int32_t inc = own;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t up = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += up;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + inc > k.w);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      const int32_t in = k.w - before - __shfl_sync(0xffffffffu, inc - own, l), per = __shfl_sync(0xffffffffu, own, l) / a.virtual_heads;
-      k.entry = e0 + l;
-      k.head = in / per;
-      k.offset = in - k.head * per;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      if (pass == 0 || a.B > 32) {
+        s.m = s.n = 0;
+        if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
+        n = units_in(a, (int64_t)s.m << a.pack_log);
+        own = sequence_cost(a, s, n, lane);
+      }
+      if (pass == 0) {
+        total += own;
+        continue;
+      }
+      const int l = lane_at(own * a.virtual_heads, k.w, before, lane);
+      if (l < 0) continue;
+      k.b = b0 + l;
+      k.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+      k.s.m = __shfl_sync(0xffffffffu, s.m, l);
+      k.s.k0 = __shfl_sync(0xffffffffu, s.k0, l);
+      k.s.n = __shfl_sync(0xffffffffu, s.n, l);
+      k.num_tiles = __shfl_sync(0xffffffffu, n, l);
       break;
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    if (pass == 0) {
+      total = __reduce_add_sync(0xffffffffu, total) * a.virtual_heads;
+      k.share = share_of(a, total);
+      k.w = (int32_t)min((int64_t)total, (int64_t)c * k.share);
+      k.w_end = k.w + min(k.share, total - k.w);
+      if (k.w >= k.w_end) return k;
+    }
+  }
+#pragma unroll 1
+  for (int32_t t0 = 0; t0 < k.num_tiles; t0 += 32) {
+    const int32_t cost = t0 + lane < k.num_tiles ? entry_cost(a, k.s, t0 + lane) : 0;
+    const int l = lane_at(cost * a.virtual_heads, k.w, before, lane);
+    if (l < 0) continue;
+    const int32_t per = __shfl_sync(0xffffffffu, cost, l);
+    k.tile = t0 + l;
+    k.head = (k.w - before) / per;
+    k.offset = k.w - before - k.head * per;
+    break;
   }
   return k;
 }
@@ -311,14 +357,8 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
   Unit x;
   x.live = 0;
 #pragma unroll 1
-  while (k.w < k.w_end && k.entry < a.entries) {  // (ends that fall, against the contract, can give more entries than there is room for)
-    int b = 0, tile = k.entry;
-    if (a.listed) {
-      const int2 at = a.list[k.entry];
-      b = at.x;
-      tile = at.y;
-    }
-    x = unit_of(a, load_seq(a, b), tile, k.head);
+  while (k.w < k.w_end && k.b < a.B) {
+    x = unit_of(a, k.s, k.tile, k.head);
     const int32_t len = max(1, x.all), off = k.offset, take = min(len - off, k.w_end - k.w);
     if (off < len) {
       cut(a, x, off, min(x.all, off + take));
@@ -340,7 +380,13 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
     k.offset = 0;
     if (++k.head == a.virtual_heads) {
       k.head = 0;
-      ++k.entry;
+      ++k.tile;
+    }
+#pragma unroll 1
+    while (k.tile == k.num_tiles && ++k.b < a.B) {
+      k.s = load_seq(a, k.b);
+      k.num_tiles = units_in(a, (int64_t)k.s.m << a.pack_log);
+      k.tile = 0;
     }
     if (off < len) return x;
     x.live = 0;
@@ -903,7 +949,6 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
 
 // The (sequence, row tile) entries of a batch, by one CTA.
 constexpr int kListThreads = 1024, kBins = 2048;
-constexpr int kAlone = 4;  // a thread deals with a sequence of so many row tiles alone, a warp with a longer one
 
 // Calls use(sequence, row tile, tiles of keys) for every entry.
 template <class Use>
@@ -987,105 +1032,6 @@ __global__ void __launch_bounds__(kListThreads) prompt_list_kernel(const PromptA
 }
 static_assert(kBins == 2 * kListThreads, "two bins a thread");
 
-// In order, for a shared call, and where each CTA's share begins (behind those: the share, and all units of work).
-__global__ void __launch_bounds__(kListThreads) prompt_share_kernel(const PromptArgs a) {
-  __shared__ int32_t sums[32];
-  __shared__ int32_t work;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int heads = a.virtual_heads;
-  if (threadIdx.x == 0) work = 0;
-  __syncthreads();
-  int32_t mine = 0;
-  each_entry(a, [&](int, int, int32_t tiles) { mine += cost_of(tiles); });
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&work, mine);
-  __syncthreads();
-  const int32_t total = work * heads, share = share_of(a, total);
-  if (threadIdx.x == 0) {
-    a.starts[a.ctas].offset = share;
-    a.starts[a.ctas + 1].offset = total;
-  }
-#pragma unroll 1
-  for (int32_t c = threadIdx.x; c < a.ctas; c += kListThreads)
-    if ((int64_t)c * share >= total) a.starts[c].entry = -1;
-  // sequences in blocks of kListThreads: the entries and the work before a thread's sequence, then its own entries
-  const int lane = threadIdx.x & 31;
-  const auto write = [&](int b, int t, int32_t e, int32_t w, int32_t cost) {
-    const int32_t lo = w * heads, hi = lo + cost * heads;
-    if (e < a.entries) a.list[e] = make_int2(b, t);
-#pragma unroll 1
-    for (int32_t c = lo / share + (lo % share ? 1 : 0); c < a.ctas && (int64_t)c * share < hi; ++c) {
-      a.starts[c].entry = e;
-      a.starts[c].head = (c * share - lo) / cost;
-      a.starts[c].offset = (c * share - lo) % cost;
-    }
-  };
-  int32_t entry0 = 0, work0 = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.B; b0 += kListThreads) {
-    const int b = b0 + threadIdx.x;
-    PromptSeq s = {0, 0, 0, 0};
-    if (b < a.B) s = load_seq(a, b);
-    const int32_t n = units_in(a, s.m << a.pack_log);
-    const auto cost = [&](const PromptSeq& o, int32_t t) {
-      return cost_of(tiles_of(a, o, min(o.m << a.pack_log, (t + 1) * a.rows_per_unit)));
-    };
-    const auto of_lane = [&](int l) {
-      PromptSeq o = {0, 0, 0, 0};
-      o.m = __shfl_sync(0xffffffffu, s.m, l);
-      o.n = __shfl_sync(0xffffffffu, s.n, l);
-      return o;
-    };
-    const uint32_t longer = __ballot_sync(0xffffffffu, n > kAlone);
-    int32_t own = 0, entries, works;
-    if (n <= kAlone)
-#pragma unroll 1
-      for (int32_t t = 0; t < n; ++t) own += cost(s, t);
-#pragma unroll 1
-    for (uint32_t left = longer; left; left &= left - 1) {
-      const int l = __ffs(left) - 1;
-      const PromptSeq o = of_lane(l);
-      const int32_t o_n = __shfl_sync(0xffffffffu, n, l);
-      int32_t sum = 0;
-#pragma unroll 1
-      for (int32_t t = lane; t < o_n; t += 32) sum += cost(o, t);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == l) own = sum;
-    }
-    const int32_t e = entry0 + block_scan(n, sums, entries);
-    int32_t w = work0 + block_scan(own, sums, works);
-    if (n <= kAlone)
-#pragma unroll 1
-      for (int32_t t = 0; t < n; ++t) {
-        const int32_t c = cost(s, t);
-        write(b, t, e + t, w, c);
-        w += c;
-      }
-#pragma unroll 1
-    for (uint32_t left = longer; left; left &= left - 1) {
-      const int l = __ffs(left) - 1;
-      const PromptSeq o = of_lane(l);
-      const int32_t o_n = __shfl_sync(0xffffffffu, n, l), o_e = __shfl_sync(0xffffffffu, e, l);
-      int32_t o_w = __shfl_sync(0xffffffffu, w, l);
-#pragma unroll 1
-      for (int32_t t0 = 0; t0 < o_n; t0 += 32) {
-        const int32_t c = t0 + lane < o_n ? cost(o, t0 + lane) : 0;
-        int32_t inc = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int32_t up = __shfl_up_sync(0xffffffffu, inc, d);
-          if (lane >= d) inc += up;
-        }
-        if (c) write(b0 + (int)(threadIdx.x & ~31u) + l, t0 + lane, o_e + t0 + lane, o_w + inc - c, c);
-        o_w += __shfl_sync(0xffffffffu, inc, 31);
-      }
-    }
-    entry0 += entries;
-    work0 += works;
-  }
-}
-
 bool encode(EncodeTiledFn enc, CUtensorMap* map, const void* p, int64_t dims, int64_t heads, int64_t head_stride, int64_t rows,
             int64_t row_stride, int box_heads, int box_rows) {
   // (a dim of one element may have any stride in the caller's tensor)
@@ -1136,8 +1082,7 @@ cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream) {
       !(keys ? encode(enc, &v, a.v, kHeadV, hk, a.v_hs, a.num_k, a.v_ts, 1, kKeys / 2) : (v = q, true)))
     return cudaErrorInvalidValue;
   if (a.listed) {
-    if (a.shared) prompt_share_kernel<<<1, kListThreads, 0, stream>>>(a);
-    else prompt_list_kernel<<<1, kListThreads, 0, stream>>>(a);
+    prompt_list_kernel<<<1, kListThreads, 0, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
