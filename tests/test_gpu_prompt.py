@@ -252,6 +252,18 @@ def test_many_sequences(seqs, most):
         check(a, p.want())
 
 
+@pytest.mark.parametrize("ctas", [1, 37, 152, 1000])
+@pytest.mark.parametrize("most", [1500, 60])
+def test_shares_of_a_large_batch(ctas, most):
+    """Shares that begin in any of a hundred sequences, empty ones and ones of many row tiles among them, with one and two lanes."""
+    rng = np.random.default_rng(most)
+    m = [int(v) for v in np.minimum(most, rng.choice([0, 1, 3, 60, 130, 700, 1500], 100, p=[.2, .3, .2, .2, .06, .02, .02]))]
+    m[0], m[31], m[32], m[-1] = 0, most, 0, most
+    n = [v + int(e) for v, e in zip(m, rng.choice([0, 5, 200], 100))]
+    p = Problem(m, n, 2, seed=21)
+    check(p.run(num_ctas=ctas), p.want())
+
+
 def test_lengths_are_read_on_the_device():
     """A call with room for more, captured, then replayed with other lengths and data: as an eager call with those."""
     import torch
