@@ -97,4 +97,13 @@ __device__ __forceinline__ int32_t units_in(const PromptArgs& a, int64_t rows) {
 // Units of work of an entry and virtual head: its tiles, at least one, and what a run costs besides.
 __device__ __forceinline__ int32_t cost_of(int32_t tiles) { return max(1, tiles) + kUnitCost; }
 
+// total + low += x, x >= 0: low keeps what total's rounding loses (exactly, as long as total is not below x; each time it is, total at
+// least doubles, so that those errors stay within 2^-22 of the end's total). A softmax sum that takes weights of about 1 one by one
+// rounds each to the last place of the total, equal ones always the same way: off by 2^-12 after 2^17 of them.
+__device__ __forceinline__ void add_keeping(float& total, float& low, float x) {
+  const float s = __fadd_rn(total, x);
+  low = __fadd_rn(low, __fsub_rn(x, __fsub_rn(s, total)));
+  total = s;
+}
+
 }  // namespace mla
