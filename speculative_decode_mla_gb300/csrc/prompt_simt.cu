@@ -7,7 +7,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Lane l holds dims l, l + 32, ... of the query, the key (192 dims) and the output (128 dims).
+// Lane l holds dims l, l + 32, ... of the query, the key (192 dims) and the output (128 dims). Sums are taken over 128 keys first and then
+// over these, so that a total of many keys does not round each of them to its own last place (as add_keeping says).
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), rows = a.num_q * a.H;
@@ -17,7 +18,17 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
   PromptSeq s;
   if (sequence_of(a, row, s) < 0) return;
   const int32_t vis = visible(a, s, (int32_t)(row - s.q0));
-  float q[6], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+  float q[6], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f, l_low = 0.f;
+  float part_o[4] = {0.f, 0.f, 0.f, 0.f}, part_l = 0.f;  // of the keys since the last whole 128
+  const auto add_part = [&] {
+    add_keeping(l, l_low, part_l);
+    part_l = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[j] += part_o[j];
+      part_o[j] = 0.f;
+    }
+  };
 #pragma unroll
   for (int j = 0; j < 6; ++j) q[j] = __bfloat162float(a.q[row * a.q_ts + h * a.q_hs + lane + 32 * j]);
   for (int64_t t = 0; t < vis; ++t) {
@@ -35,10 +46,18 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const PromptArgs 
     const float top = fmaxf(m, x);
     const float keep = m == top ? 1.f : expf(m - top), p = expf(x - (top == -INFINITY ? 0.f : top));
     m = top;
-    l = fmaf(l, keep, p);
+    l *= keep;
+    l_low *= keep;
+    part_l = fmaf(part_l, keep, p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(o[j], keep, p * __bfloat162float(v[lane + 32 * j]));
+    for (int j = 0; j < 4; ++j) {
+      o[j] *= keep;
+      part_o[j] = fmaf(part_o[j], keep, p * __bfloat162float(v[lane + 32 * j]));
+    }
+    if (t % 128 == 127) add_part();
   }
+  add_part();
+  l += l_low;
   const float inv = l == 0.f ? 0.f : 1.f / l, lse = l == 0.f ? -INFINITY : m + logf(l);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -40,14 +40,14 @@ def scores_of(kind, n):
 
 @pytest.mark.parametrize("kind", ["equal", "spread"])
 @pytest.mark.parametrize("m,n,how", [(1, 131072 + 37, "one cta"), (200, 70001, "one cta"), (1, 131072 + 37, "shared"), (200, 70001, "shared"),
-                                     (608 * 256, 66000, "units")])
+                                     (608 * 256, 66000, "units"), (3, 70001, "simt")])
 def test_sums_over_many_keys(m, n, how, kind):
     import torch
     import speculative_decode_mla_gb300 as lib
     q, k, kr, v = inputs(m, n, scores_of(kind, n))
     ends = lambda e: to_dev(np.array([0, e], np.int32))
     out, lse = lib.prompt_attn(q, k, kr, v, ends(m), ends(n), max_q_len=m, max_k_len=n, causal=False, softmax_scale=1.0,
-                               num_ctas=1 if how == "one cta" else 0, out_dtype=lib.MLA_DTYPE_F32)
+                               num_ctas=1 if how == "one cta" else 0, out_dtype=lib.MLA_DTYPE_F32, flags=lib.MLA_FLAG_SIMT if how == "simt" else 0)
     assert (out == out[:1]).all() and (lse == lse[0]).all() or how == "shared"     # equal queries (parts may end inside a row tile)
     host = lambda t: t.double().cpu().numpy()
     o, l, spread, size = oracle.prompt_attn(host(q[:1]), host(k), host(kr), host(v), [0, 1], [0, n], causal=False, scale=1.0)
