@@ -682,7 +682,8 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
     q: bf16 [num_q, H, 192]; k_nope, v: bf16 [num_k, Hk, 128], H a multiple of Hk; k_rope: bf16 [num_k, 64], shared by the heads
     (all may be strided in multiples of 8 elements, dims contiguous); cu_q, cu_k: int32 [B + 1], where the sequences' queries and
     keys begin and end (cu_k None: the same as cu_q). A sequence's queries are the last of its places. max_q_len, max_k_len: upper bounds
-    of their lengths (max_k_len None: max_q_len). Returns (out [num_q, H, 128], lse [num_q, H]); rows outside the sequences are left
+    of their lengths, behind which a sequence is cut off (max_k_len None: max_q_len where cu_k is None too, else the rows of k_nope, which no
+    sequence has more of; a closer bound may get a better plan). Returns (out [num_q, H, 128], lse [num_q, H]); rows outside the sequences are left
     as they were.
     """
     import torch
@@ -698,8 +699,9 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
     ends = cu_q.shape[0]
     _check_tensor("cu_q", cu_q, i32, (ends,), dev)
     if cu_k is None:
-        cu_k = cu_q
+        cu_k, most_k = cu_q, max_q_len
     else:
+        most_k = nk
         _check_tensor("cu_k", cu_k, i32, (ends,), dev)
     if dev_status is not None:
         _check_tensor("dev_status", dev_status, i32, (1,), dev)
@@ -708,7 +710,7 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
     with here:
         # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
         desc, need = _prompt_desc(
-            dev, ends - 1, heads, hk, int(max_q_len), int(max_q_len if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
+            dev, ends - 1, heads, hk, int(max_q_len), int(most_k if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
             int(DEFAULT_FLAGS if flags is None else flags), int(num_ctas), float(softmax_scale), nq, nk, *q.stride()[:2],
             *k_nope.stride()[:2], k_rope.stride(0), *v.stride()[:2])
         if out is None:

@@ -1,0 +1,48 @@
+"""The bounds that a caller of mla_prompt_attn names (include/mla_prompt.h), and what is made of them where they are left out."""
+import numpy as np
+import pytest
+
+from _helpers import to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from speculative_decode_mla_gb300 import _build
+    _build.build()
+
+
+def ints(v):
+    return to_dev(np.asarray(v, np.int32))
+
+
+def problem(nq, nk, heads=2, seed=1):
+    import torch
+    rng = np.random.default_rng(seed)
+    normal = lambda *shape: torch.from_numpy(rng.normal(size=shape).astype(np.float32)).to(torch.bfloat16).cuda()
+    return dict(q=normal(nq, heads, 192), k_nope=normal(nk, heads, 128), k_rope=normal(nk, 64), v=normal(nk, heads, 128))
+
+
+@pytest.mark.parametrize("m,n", [([17], [900]), ([1, 1, 1], [300, 5, 140]), ([40, 3], [40, 3]), ([9, 4], [3, 0])])
+def test_keys_of_their_own_are_all_read_without_a_bound(m, n):
+    """cu_k given and max_k_len not: as with the bound named, whatever the queries' bound is."""
+    import torch
+    import speculative_decode_mla_gb300 as lib
+    p = problem(sum(m), sum(n))
+    cu_q, cu_k = (ints(np.concatenate([[0], np.cumsum(v)])) for v in (m, n))
+    out, lse = lib.prompt_attn(**p, cu_q=cu_q, cu_k=cu_k, max_q_len=max(m))
+    want = lib.prompt_attn(**p, cu_q=cu_q, cu_k=cu_k, max_q_len=max(m), max_k_len=sum(n))
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    plain = lib.prompt_attn(**p, cu_q=cu_q, cu_k=cu_k, max_q_len=max(m), max_k_len=sum(n), flags=lib.MLA_FLAG_SIMT)
+    seen = torch.isfinite(plain[1])
+    assert torch.equal(seen, torch.isfinite(lse)) and torch.allclose(lse[seen], plain[1][seen], atol=2e-4)
+
+
+def test_without_keys_of_their_own_the_queries_bound_holds():
+    import torch
+    import speculative_decode_mla_gb300 as lib
+    p = problem(70, 70)
+    out, lse = lib.prompt_attn(**p, cu_q=ints([0, 30, 70]), max_q_len=40)
+    want = lib.prompt_attn(**p, cu_q=ints([0, 30, 70]), cu_k=ints([0, 30, 70]), max_q_len=40, max_k_len=40)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
