@@ -4,6 +4,12 @@
 
 #include "prompt.cuh"
 
+// Cycles after which a wait of the attention kernel gives up, about 2 s. (A build may name fewer, to see what a call leaves behind whose
+// waits run out.)
+#ifndef MLA_PROMPT_WAIT_CYCLES
+#define MLA_PROMPT_WAIT_CYCLES 4000000000ll
+#endif
+
 namespace mla {
 namespace {
 
@@ -175,6 +181,7 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
   a.debug = debug ? 1 : 0;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
+  a.wait_cycles = MLA_PROMPT_WAIT_CYCLES;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;

@@ -45,6 +45,7 @@ struct PromptArgs {
   int32_t causal, shared, ctas, rows_per_unit, listed, head_group, out_f32, debug;
   int32_t out_32;     // out is aligned to 32 bytes
   float scale, scale_log2;
+  int64_t wait_cycles;  // after which a wait of the attention kernel gives up
 };
 
 cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t stream);

@@ -33,8 +33,9 @@
 // tokens after 16 Ki, 64 heads, 94 to 97 us, 5.6 TB/s. By beginnings and ends of units in batches of short prompts: 24 of 61 to 2048
 // tokens, 16 heads, 109 us, 0.75 PFLOP/s.
 //
-// Every wait is bounded (about 2 s). On a timeout the kernel stops issuing work, drains what is in flight, reports
-// MLA_CHECK_TIMEOUT, gives its rows a NaN lse and exits.
+// Every wait is bounded (about 2 s). When one runs out its CTA stops issuing work, drains what is in flight, reports MLA_CHECK_TIMEOUT,
+// gives a NaN lse to the rows of its last two units and of those that it had claimed, or had as its share, and not begun, and exits; a
+// row that is merged from such a part is NaN. Rows of units before those are as they should be, and other CTAs go on.
 #include <atomic>
 
 #include "prompt.cuh"
@@ -118,6 +119,10 @@ __device__ __forceinline__ void mma_smem_a(uint32_t d_tmem, uint32_t a_low, uint
       "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
+// Takes bytes that a barrier was told of and that nobody will load off its phase.
+__device__ __forceinline__ void mbar_forget_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -168,12 +173,17 @@ __device__ __forceinline__ uint32_t probe4(uint32_t b0, uint32_t p0, uint32_t b1
 }
 // A wait of one thread. Its loop is a function where there are two lanes: one at each place would fill the instruction cache. (16 heads
 // of 4096 rows and keys: 122.6 us, 123.9 with a loop at each place. Calls of one lane lose 0.3 us by the call's time.)
-__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) { return wait_bar(bar, parity, abort_flag); }
-template <bool ONE>
-__device__ __forceinline__ bool wait_thread(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return ONE ? wait_bar(bar, parity, abort_flag) : mbar_test(bar, parity) || wait_on(bar, parity, abort_flag);
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, long long limit) {
+  return wait_bar(bar, parity, abort_flag, false, limit);
 }
-// A wait after an abort, for copies and MMAs that are in flight: bounded by its own clock.
+template <bool ONE>
+__device__ __forceinline__ bool wait_thread(const PromptArgs& a, uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return ONE ? wait_bar(bar, parity, abort_flag, false, a.wait_cycles) : mbar_test(bar, parity) || wait_on(bar, parity, abort_flag, a.wait_cycles);
+}
+__device__ __forceinline__ bool wait_warp(const PromptArgs& a, uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return mla::wait_warp(bar, parity, abort_flag, false, a.wait_cycles);
+}
+// A wait for copies and MMAs that are in flight when a thread is done or gives up: bounded by its own clock.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
   const long long start = clock64();
   while (!mbar_test(bar, parity) && clock64() - start < kTimeoutCycles) {
@@ -216,6 +226,18 @@ __device__ __forceinline__ void cut(const PromptArgs& a, Unit& x, int32_t t0, in
   x.t0 = t0;
   x.tiles[0] = x.all ? max(0, min(t1, tiles_of(a, x.s, min((int64_t)x.rows, mid))) - t0) : 0;
   x.tiles[1] = a.rows_per_unit > kRows && x.rows > mid ? t1 - t0 : 0;
+}
+// Where row i of a unit, or of its part, has its lse.
+__device__ __forceinline__ float* lse_at(const PromptArgs& a, const Unit& x, int i) {
+  const int at = x.row0 + i;
+  return x.part >= 0 ? a.part_lse + (int64_t)x.part * a.rows_per_unit + i
+                     : a.lse + (int64_t)(x.s.q0 + (at >> a.pack_log)) * a.H + x.h + (at & (a.pack - 1));
+}
+// Says of a unit's rows that they were not computed: a NaN lse (and, of parts, NaN rows when they are merged). Rows first, first + step, ...
+__device__ __forceinline__ void give_up(const PromptArgs& a, const Unit& x, int first, int step) {
+  const int rows = min(a.rows_per_unit, x.rows - x.row0);
+#pragma unroll 1
+  for (int i = first; i < rows; i += step) *lse_at(a, x, i) = NAN;
 }
 // Unit number u of a call that is not shared (virtual heads in groups of a.head_group; in a group by row tile, then head), found in
 // steps whose reads of memory wait for each other: a step's results are used by the next one, some tiles later.
@@ -399,9 +421,34 @@ __device__ __forceinline__ Unit next_part(const PromptArgs& a, Walk& k, int c, P
   return x;
 }
 
+// What a CTA gives up when a wait has run out: the rest of its share; a unit that it has claimed; the units that its roles were told of last,
+// which may not be done (the loader waits for all others' end of the one before those). Functions, since code that is hardly ever run costs
+// the calls of one lane 1% where it stands in the kernel (64 single tokens of 16 heads: 114.1 us, 115.6 so).
+__device__ __noinline__ void give_up_share(const PromptArgs& a, Walk walk, int c) {
+  PromptMerge merge;
+#pragma unroll 1
+  while (true) {
+    const Unit x = next_part(a, walk, c, &merge);
+    if (!x.live) break;
+    give_up(a, x, 0, 1);
+  }
+}
+__device__ __noinline__ void give_up_unit(const PromptArgs& a, Place place) {
+  read_ends(a, place);
+  give_up(a, unit_at(a, place), 0, 1);
+}
+__device__ __noinline__ void give_up_last(const PromptArgs& a, const uint32_t* units, int threads) {
+  if (threadIdx.x == 0) report(a.dev_status, a.dev_status != nullptr, MLA_CHECK_TIMEOUT);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const Unit& x = *reinterpret_cast<const Unit*>(units + i * kUnitWords);
+    if (x.live) give_up(a, x, threadIdx.x, threads);
+  }
+}
+
 template <bool ONE>
 __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
-    prompt_tc_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+    prompt_tc_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_kr, const __grid_constant__ CUtensorMap map_v) {
   using L = Layout<ONE>;
   constexpr uint32_t kSlots = L::slots;
@@ -433,6 +480,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     mbar_init(bar(L::next), 1);
     mbar_init(bar(L::drain), 1);
     *abort_flag = 0;
+    unit_slot(0)->live = unit_slot(1)->live = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == L::load_warp && elect_one()) {
@@ -468,7 +516,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         if (blocks >= kSlots) {
           const uint32_t old = blocks - kSlots, group = 2 * (old / kTileBlocks) + (old % kTileBlocks >= 3);
           for (; freed <= group; ++freed)
-            if (!wait_thread<ONE>(bar(L::freed + (freed & 7)), (freed >> 3) & 1, abort_flag)) return false;
+            if (!wait_thread<ONE>(a, bar(L::freed + (freed & 7)), (freed >> 3) & 1, abort_flag)) return false;
         }
         const uint32_t dst = base + L::ring + (blocks % kSlots) * kBlock;
         tma_load3(dst, map, x, y, z, bar(landed));
@@ -478,16 +526,29 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       };
       bool next_asked = false;
       uint32_t n_unit = 0, n_asked = 0;
-      bool ok = true, more = true;  // more: there is a next unit, at `place`
+      bool ok = true, more = true;  // more: there is a next unit, at `place`, which no other role has heard of
       Place place = {};
       if (!a.shared) {
         place = place_of(a, blockIdx.x);
         read_ends(a, place);
       }
+      const auto take_answer = [&] {
+        uint32_t got, id;
+        asm volatile(
+            "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b64 lo, hi;\n"
+            "ld.shared.v2.b64 {lo, hi}, [%2];\nmov.b128 h, {lo, hi};\n"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
+            : "=r"(got), "=r"(id)
+            : "r"(base + L::answer)
+            : "memory");
+        more = got != 0;
+        if (more) place = place_of(a, id);
+      };
       PromptMerge merge = {};
       while (ok) {
         const int slot = n_unit & 1;
-        if (n_unit >= 2 && !wait_thread<ONE>(bar(L::unit_empty + slot), ((n_unit >> 1) - 1) & 1, abort_flag)) break;
+        if (n_unit >= 2 && !wait_thread<ONE>(a, bar(L::unit_empty + slot), ((n_unit >> 1) - 1) & 1, abort_flag)) break;
         Unit x;
         x.live = 0;
         if (a.shared) {
@@ -495,6 +556,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           if (n_unit == 0) a.merges[blockIdx.x] = merge;
         } else if (more) {
           x = unit_at(a, place);
+          more = false;
         }
         // (a unit without rows, where the lengths leave fewer than the call has room for, is passed over)
         const bool none = !a.shared && x.live && x.rows == 0;
@@ -515,7 +577,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         const int n = max(x.tiles[0], x.tiles[1]);
         const auto load_q = [&](int r) {
           if (x.tiles[r] == 0) return true;
-          if (q_loads[r] > 0 && !wait_thread<ONE>(bar(L::q_empty + r), (q_loads[r] - 1) & 1, abort_flag)) return false;
+          if (q_loads[r] > 0 && !wait_thread<ONE>(a, bar(L::q_empty + r), (q_loads[r] - 1) & 1, abort_flag)) return false;
           const uint32_t full = bar(L::q_full + r);
           mbar_arrive_expect_tx(full, kQBytes);
           for (int i = 0; i < 3; ++i)
@@ -535,42 +597,42 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
             if (!ok) break;
             mbar_arrive_expect_tx(bar(vals), 2 * kBlock);
             ok = load_block(&map_v, 0, x.g, at, vals, true) && load_block(&map_v, 0, x.g, at + 64, vals, true);
-            ++tiles;
+            if (ok) ++tiles;
           }
           if (a.shared || !ok) continue;
           if (j == 0) {
-            ok = wait_thread<ONE>(bar(L::next), n_asked & 1, abort_flag);
+            ok = wait_thread<ONE>(a, bar(L::next), n_asked & 1, abort_flag);
             if (!ok) break;
             ++n_asked;
             next_asked = false;
-            uint32_t got, id;
-            asm volatile(
-                "{\n.reg .b128 h;\n.reg .pred p;\n.reg .b64 lo, hi;\n"
-                "ld.shared.v2.b64 {lo, hi}, [%2];\nmov.b128 h, {lo, hi};\n"
-                "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
-                "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}"
-                : "=r"(got), "=r"(id)
-                : "r"(base + L::answer)
-                : "memory");
-            more = got != 0;
-            if (more) place = place_of(a, id);
+            take_answer();
           } else if (j == 1 && more) {
             read_ends(a, place);
           }
         }
         if (!none) ++n_unit;
       }
-      if (*abort_flag) {  // what is in flight lands before the CTA ends
-        if (next_asked) drain_bar(bar(L::next), n_asked & 1);
-        // (a tile begun but not loaded whole never completes its phase: its wait runs out)
-        for (uint32_t i = tiles > 2 ? tiles - 3 : 0; i <= tiles; ++i) {
-          if (i == tiles && blocks <= kTileBlocks * tiles) break;
-          drain_bar(bar(L::keys + (i & 3)), (i >> 2) & 1);
-          drain_bar(bar(L::vals + (i & 3)), (i >> 2) & 1);
+      // What is in flight lands before the CTA ends, also where another role gives up after this one has left.
+      if (next_asked) drain_bar(bar(L::next), n_asked & 1);
+      const uint32_t begun = blocks - kTileBlocks * tiles;  // blocks of a tile that was not loaded whole
+      if (begun > 0) {
+        if (begun != 3) mbar_forget_tx(bar((begun < 3 ? L::keys : L::vals) + (tiles & 3)), ((begun < 3 ? 3 : 5) - begun) * kBlock);
+        drain_bar(bar(L::keys + (tiles & 3)), (tiles >> 2) & 1);
+        if (begun > 3) drain_bar(bar(L::vals + (tiles & 3)), (tiles >> 2) & 1);
+      }
+      for (uint32_t i = tiles > 2 ? tiles - 3 : 0; i < tiles; ++i) {
+        drain_bar(bar(L::keys + (i & 3)), (i >> 2) & 1);
+        drain_bar(bar(L::vals + (i & 3)), (i >> 2) & 1);
+      }
+      for (int r = 0; r < 2; ++r)
+        if (q_loads[r]) drain_bar(bar(L::q_full + r), (q_loads[r] - 1) & 1);
+      if (*abort_flag) {  // what this CTA was to compute and no other role has heard of
+        if (a.shared) {
+          give_up_share(a, walk, blockIdx.x);
+        } else {
+          if (next_asked && mbar_test(bar(L::next), n_asked & 1)) take_answer();
+          if (more) give_up_unit(a, place);
         }
-        for (int r = 0; r < 2; ++r)
-          if (q_loads[r]) drain_bar(bar(L::q_full + r), (q_loads[r] - 1) & 1);
-        report(a.dev_status, a.dev_status != nullptr, MLA_CHECK_TIMEOUT);
       }
     }
     __syncwarp();
@@ -590,7 +652,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       uint32_t keys_seen = 0, vals_seen = 0;       // tiles whose keys, values are known to have landed
       uint32_t p_seen = 0;                         // bits of the next step's halves of P that are known to be there
       bool issued = false;
-      const auto wait = [&](int b, uint32_t parity) { return wait_thread<ONE>(bar(b), parity, abort_flag); };
+      const auto wait = [&](int b, uint32_t parity) { return wait_thread<ONE>(a, bar(b), parity, abort_flag); };
       const auto block_at = [&](uint32_t tile, int i) { return base + L::ring + (tile * kTileBlocks + i) % kSlots * kBlock; };
       // S buffer s = Q of lane r times the keys of a tile; `ask` asks for what comes next.
       const auto scores = [&](int r, int s, uint32_t tile, bool last, auto ask) {
@@ -696,7 +758,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         if (!ok) break;
         tiles += n;
       }
-      if (*abort_flag && issued) {
+      if (issued) {  // (also where another role gives up after this one has left)
         mma_commit(bar(L::drain));
         drain_bar(bar(L::drain), 0);
       }
@@ -711,7 +773,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
     bool ok = true;
     for (uint32_t n_unit = 0; ok; ++n_unit) {
       const int slot = n_unit & 1;
-      if (!wait_warp(bar(L::unit + slot), (n_unit >> 1) & 1, abort_flag)) break;
+      if (!wait_warp(a, bar(L::unit + slot), (n_unit >> 1) & 1, abort_flag)) break;
       const Unit& x = *unit_slot(slot);
       if (!x.live) break;
       const int n = r ? x.tiles[1] : x.tiles[0], unit_tiles = max(x.tiles[0], x.tiles[1]), other = r ? x.tiles[0] : x.tiles[1];
@@ -724,13 +786,13 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
       for (int j = 0; j < n; ++j) {
         const int buf = ONE ? (int)(tile_uses & 1) : r, tile = t0 + j;
         const uint32_t tS = tmem + lanes + kColS + 128 * buf;
-        const auto scores_there = [&] { return wait_warp(bar(L::s + buf), (ONE ? tile_uses >> 1 : tile_uses) & 1, abort_flag); };
+        const auto scores_there = [&] { return wait_warp(a, bar(L::s + buf), (ONE ? tile_uses >> 1 : tile_uses) & 1, abort_flag); };
         if (tile >= special && (r == 0 || j >= other)) {
           // the first lane that uses the tile looks through its values: thread `row` has key `row`
           // (A barrier may be asked for a phase only when the one before it is over: here that of four tiles ago, whose block the tile
           // after it has taken by now.)
           const uint32_t here = tiles + j, block = kTileBlocks * here + 3 + (row >> 6);
-          if ((j == 0 && !scores_there()) || !wait_warp(bar(L::vals + (here & 3)), (here >> 2) & 1, abort_flag)) {
+          if ((j == 0 && !scores_there()) || !wait_warp(a, bar(L::vals + (here & 3)), (here >> 2) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -807,7 +869,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           l_low *= keep;
           if (j > 0) {
             // (with two lanes these scores were issued after the product before, so that it is over)
-            if (ONE && !wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) {
+            if (ONE && !wait_warp(a, bar(L::o + r), (tile_uses - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
@@ -861,7 +923,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
           TMEM_ST32(tS + 32 * half, w);
           // With two S buffers the product before the last may not be over when the last one's weights are there. It has to be before
           // these are announced: afterwards the parity could not tell whether one more, two more or none has ended.
-          if (ONE && half == 1 && j == n - 1 && j > 0) ok = wait_warp(bar(L::o + r), (tile_uses - 1) & 1, abort_flag);
+          if (ONE && half == 1 && j == n - 1 && j > 0) ok = wait_warp(a, bar(L::o + r), (tile_uses - 1) & 1, abort_flag);
           announce(half);
         }
         if (!ok) break;
@@ -870,18 +932,14 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
         ++tile_uses;
       }
       // the last product of this lane, then O / l
-      if (ok && n > 0) ok = wait_warp(bar(L::o + r), (ONE ? tile_uses - 1 : units_done) & 1, abort_flag);
+      if (ok && n > 0) ok = wait_warp(a, bar(L::o + r), (ONE ? tile_uses - 1 : units_done) & 1, abort_flag);
       units_done += n > 0;
       const int64_t rh = (int64_t)(x.s.q0 + (at >> a.pack_log)) * a.H + x.h + (at & (a.pack - 1));
       const int64_t part = (int64_t)x.part * a.rows_per_unit + r * kRows + row;
-      float* const lse_at = x.part >= 0 ? a.part_lse + part : a.lse + rh;
-      if (!ok) {
-        if (real) *lse_at = NAN;
-        break;
-      }
+      if (!ok) break;
       tc_fence_after();
       const float sum = l + l_low, inv = sum == 0.f ? 0.f : 1.f / sum;
-      if (real) *lse_at = sum == 0.f ? -INFINITY : m * a.scale + __logf(sum);
+      if (real) *(x.part >= 0 ? a.part_lse + part : a.lse + rh) = sum == 0.f ? -INFINITY : m * a.scale + __logf(sum);
       if (x.part >= 0 || a.out_f32) {
         float* const dst = x.part >= 0 ? a.part_o + part * kHeadV : static_cast<float*>(a.out) + rh * kHeadV;
 #pragma unroll 1
@@ -952,6 +1010,7 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*abort_flag) give_up_last(a, reinterpret_cast<const uint32_t*>(unit_slot(0)), L::threads);
   if (warp == L::mma_warp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
