@@ -171,17 +171,31 @@ __device__ __forceinline__ uint32_t probe4(uint32_t b0, uint32_t p0, uint32_t b1
       : "memory");
   return r0 | r1 | r2 | r3;
 }
+// A wait that gives up after so many cycles, or when another role has: false then. (The first probe goes out before the clock is read.)
+__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, long long limit) {
+  if (mbar_test(bar, parity)) return true;
+  const long long start = clock64();
+  while (true) {
+    if (mbar_test(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - start > limit) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 // A wait of one thread. Its loop is a function where there are two lanes: one at each place would fill the instruction cache. (16 heads
 // of 4096 rows and keys: 122.6 us, 123.9 with a loop at each place. Calls of one lane lose 0.3 us by the call's time.)
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, long long limit) {
-  return wait_bar(bar, parity, abort_flag, false, limit);
+  return wait_until(bar, parity, abort_flag, limit);
 }
 template <bool ONE>
 __device__ __forceinline__ bool wait_thread(const PromptArgs& a, uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return ONE ? wait_bar(bar, parity, abort_flag, false, a.wait_cycles) : mbar_test(bar, parity) || wait_on(bar, parity, abort_flag, a.wait_cycles);
+  return ONE ? wait_until(bar, parity, abort_flag, a.wait_cycles) : mbar_test(bar, parity) || wait_on(bar, parity, abort_flag, a.wait_cycles);
 }
+// The same of every lane of a warp; the result is uniform across the warp.
 __device__ __forceinline__ bool wait_warp(const PromptArgs& a, uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return mla::wait_warp(bar, parity, abort_flag, false, a.wait_cycles);
+  return __all_sync(0xffffffffu, wait_until(bar, parity, abort_flag, a.wait_cycles));
 }
 // A wait for copies and MMAs that are in flight when a thread is done or gives up: bounded by its own clock.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {

@@ -47,7 +47,7 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 // A probe of an mbarrier costs over a hundred cycles even when the phase has completed, and
 // reading the clock costs some too: the first probe goes out before the clock is read.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                         bool cluster_scope = false, long long limit = kTimeoutCycles) {
+                                         bool cluster_scope = false) {
   if (cluster_scope) {
     if (mbar_test_cluster(bar, parity)) {
       asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
@@ -67,7 +67,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
       return true;
     }
     if (*abort_flag) return false;
-    if (clock64() - start > limit) {
+    if (clock64() - start > kTimeoutCycles) {
       *abort_flag = 1;
       return false;
     }
@@ -75,8 +75,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 }
 // The same wait taken by every lane of a warp; the result is uniform across the warp.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                          bool cluster_scope = false, long long limit = kTimeoutCycles) {
-  const bool ok = wait_bar(bar, parity, abort_flag, cluster_scope, limit);
+                                          bool cluster_scope = false) {
+  const bool ok = wait_bar(bar, parity, abort_flag, cluster_scope);
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t cta) {
