@@ -4,10 +4,14 @@
 
 #include "prompt.cuh"
 
-// Cycles after which a wait of the attention kernel gives up, about 2 s. (A build may name fewer, to see what a call leaves behind whose
-// waits run out.)
+// Cycles after which a wait of the attention kernel gives up: about 2 s, and ten times what a tile takes (3000 to 4300) for each tile of a
+// sequence's keys, since a role without work in a unit waits for the end of that unit. (A build may name others, to see what a call leaves
+// behind whose waits run out.)
 #ifndef MLA_PROMPT_WAIT_CYCLES
 #define MLA_PROMPT_WAIT_CYCLES 4000000000ll
+#endif
+#ifndef MLA_PROMPT_WAIT_CYCLES_A_TILE
+#define MLA_PROMPT_WAIT_CYCLES_A_TILE 32768
 #endif
 
 namespace mla {
@@ -52,6 +56,8 @@ int64_t entries_of(const mla_prompt_desc& d, int64_t rows) {
   const int64_t a = any_entries(d, rows), b = d.num_q * pack_of(d) / rows + d.num_seqs;
   return a < b ? a : b;
 }
+// Tiles of a sequence's keys, at most.
+int64_t key_tiles(const mla_prompt_desc& d) { return cdiv(d.max_k_len < d.num_k ? d.max_k_len : d.num_k, kPromptTile); }
 int64_t pad(int64_t bytes) { return cdiv(bytes, 256) * 256; }
 
 }  // namespace
@@ -65,7 +71,7 @@ extern "C" int mla_prompt_plan(const mla_prompt_desc* d, int32_t num_sms, mla_pr
   if (!plan || num_sms < 1) return MLA_ERR_INVALID_ARGUMENT;
   mla_prompt_plan_t p;
   memset(&p, 0, sizeof p);
-  const int64_t most_k = d->max_k_len < d->num_k ? d->max_k_len : d->num_k, tiles = cdiv(most_k, kPromptTile);
+  const int64_t tiles = key_tiles(*d);
   p.pack = pack_of(*d);
   if (d->flags & MLA_FLAG_SIMT) {
     p.kernel = 1;
@@ -181,7 +187,7 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
   a.debug = debug ? 1 : 0;
   a.scale = d->softmax_scale;
   a.scale_log2 = d->softmax_scale * 1.4426950408889634f;
-  a.wait_cycles = MLA_PROMPT_WAIT_CYCLES;
+  a.wait_cycles = MLA_PROMPT_WAIT_CYCLES + (int64_t)MLA_PROMPT_WAIT_CYCLES_A_TILE * key_tiles(*d);
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (debug && cudaMemsetAsync(dev_status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;

@@ -33,7 +33,7 @@
 // tokens after 16 Ki, 64 heads, 94 to 97 us, 5.6 TB/s. By beginnings and ends of units in batches of short prompts: 24 of 61 to 2048
 // tokens, 16 heads, 109 us, 0.75 PFLOP/s.
 //
-// Every wait is bounded (about 2 s). When one runs out its CTA stops issuing work, drains what is in flight, reports MLA_CHECK_TIMEOUT,
+// Every wait is bounded (about 2 s, and more for many keys). When one runs out its CTA stops issuing work, drains what is in flight, reports MLA_CHECK_TIMEOUT,
 // gives a NaN lse to the rows of its last two units and of those that it had claimed, or had as its share, and not begun, and exits; a
 // row that is merged from such a part is NaN. Rows of units before those are as they should be, and other CTAs go on.
 #include <atomic>
