@@ -96,7 +96,7 @@ typedef struct mla_prompt_desc {
   int32_t out_dtype;       /* MLA_DTYPE_BF16 or MLA_DTYPE_F32 */
   int32_t flags;           /* MLA_FLAG_DEBUG_CHECKS, MLA_FLAG_SIMT */
   int32_t num_ctas;        /* 0: planner decides; > 0: the work is shared out evenly over this many CTAs (at most 1024) */
-  float softmax_scale;     /* finite and > 0 */
+  float softmax_scale;     /* > 0 and at most 2^127 */
   int64_t num_q, num_k;    /* rows of q (and out, lse), and of k_nope, k_rope and v; 0 .. 2^30 */
   int64_t q_token_stride, q_head_stride;  /* all strides: multiples of 8, from 8 to 2^38 */
   int64_t k_token_stride, k_head_stride;

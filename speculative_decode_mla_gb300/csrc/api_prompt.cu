@@ -34,7 +34,8 @@ int check_prompt(const mla_prompt_desc* d) {
   if (d->out_dtype != MLA_DTYPE_BF16 && d->out_dtype != MLA_DTYPE_F32) return MLA_ERR_INVALID_ARGUMENT;
   if (d->flags & ~(MLA_FLAG_DEBUG_CHECKS | MLA_FLAG_SIMT)) return MLA_ERR_INVALID_ARGUMENT;
   if (d->num_ctas < 0 || d->num_ctas > kMaxPromptCtas) return MLA_ERR_INVALID_ARGUMENT;
-  if (!isfinite(d->softmax_scale) || !(d->softmax_scale > 0.f)) return MLA_ERR_INVALID_ARGUMENT;
+  // (the kernel works with the scale times log2 e, which has to be finite too)
+  if (!(d->softmax_scale > 0.f) || !(d->softmax_scale <= 0x1p127f)) return MLA_ERR_INVALID_ARGUMENT;
   // the stride of a dim with one element is not used
   if ((d->num_q > 1 && !good_stride(d->q_token_stride)) || (d->num_heads > 1 && !good_stride(d->q_head_stride)))
     return MLA_ERR_INVALID_ARGUMENT;

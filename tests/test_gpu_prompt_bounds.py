@@ -46,3 +46,23 @@ def test_without_keys_of_their_own_the_queries_bound_holds():
     out, lse = lib.prompt_attn(**p, cu_q=ints([0, 30, 70]), max_q_len=40)
     want = lib.prompt_attn(**p, cu_q=ints([0, 30, 70]), cu_k=ints([0, 30, 70]), max_q_len=40, max_k_len=40)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("flags", ["simt", "tc"])
+@pytest.mark.parametrize("log2_scale", [127, 100, 0, -100, -149])
+def test_scales_to_the_ends_of_their_range(log2_scale, flags):
+    """Queries that undo the scale as far as bf16 goes: scores as float64 has them (powers of two leave every other rounding as it is)."""
+    import oracle
+    import speculative_decode_mla_gb300 as lib
+    p = problem(150, 400, heads=1, seed=3)
+    p["q"].mul_(2.0 ** max(-60, min(90, -log2_scale // 2)))
+    for k in ("k_nope", "k_rope"):
+        p[k].mul_(2.0 ** max(-60, min(30, -log2_scale - (-log2_scale // 2) - 3)))
+    scale = 2.0 ** log2_scale
+    out, lse = lib.prompt_attn(**p, cu_q=ints([0, 150]), cu_k=ints([0, 400]), max_q_len=150, max_k_len=400, softmax_scale=scale,
+                               flags=lib.MLA_FLAG_SIMT if flags == "simt" else 0)
+    host = lambda t: t.double().cpu().numpy()
+    o, l, spread, size = oracle.prompt_attn(*(host(p[k]) for k in ("q", "k_nope", "k_rope", "v")), [0, 150], [0, 400], causal=True, scale=scale)
+    e = 256 * 2.0 ** -23 * size      # the tolerances of test_gpu_prompt.py
+    assert (np.abs(host(lse) - l) <= e + 2.0 ** -20 * (1 + np.abs(l))).all()
+    assert (np.abs(host(out) - o) <= (2.0 ** -8 + 2.5 * e + 2.0 ** -19)[..., None] * spread + 2.0 ** -8 * np.abs(o) + 1e-30).all()
