@@ -197,6 +197,8 @@ extern "C" int mla_prompt_attn(const mla_prompt_desc* d, const void* q, const vo
     if (p.shared && launch_prompt_merge(a, s) != cudaSuccess) return MLA_ERR_CUDA;
   }
   if (!debug) return MLA_OK;
+  // the tcgen05 kernels look at every sequence, the SIMT kernel at those that a row belongs to
+  if ((p.kernel == 1 || p.ctas == 0) && launch_prompt_check(a, s) != cudaSuccess) return MLA_ERR_CUDA;
   mla_verify_desc checks = {};
   checks.flags = d->flags;
   return finish_debug(&checks, dev_status, s);

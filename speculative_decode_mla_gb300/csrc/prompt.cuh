@@ -51,6 +51,7 @@ struct PromptArgs {
 cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_prompt_tc(const PromptArgs& a, cudaStream_t stream);
 cudaError_t launch_prompt_merge(const PromptArgs& a, cudaStream_t stream);
+cudaError_t launch_prompt_check(const PromptArgs& a, cudaStream_t stream);  // under debug: reports bad ends of any sequence
 
 // A sequence's queries [q0, q0 + m) and keys [k0, k0 + n), clamped into the tensors and the host's bounds.
 struct PromptSeq {

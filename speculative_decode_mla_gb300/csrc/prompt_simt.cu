@@ -137,7 +137,17 @@ __global__ void __launch_bounds__(kThreads) prompt_merge_kernel(const PromptArgs
   }
 }
 
+__global__ void __launch_bounds__(kThreads) prompt_check_kernel(const PromptArgs a) {
+  const int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (b < a.B) load_seq(a, (int)b);
+}
+
 }  // namespace
+
+cudaError_t launch_prompt_check(const PromptArgs& a, cudaStream_t stream) {
+  prompt_check_kernel<<<(unsigned)(((int64_t)a.B + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_prompt_simt(const PromptArgs& a, cudaStream_t stream) {
   const int64_t blocks = (a.num_q * a.H + kWarps - 1) / kWarps;

@@ -66,3 +66,27 @@ def test_scales_to_the_ends_of_their_range(log2_scale, flags):
     e = 256 * 2.0 ** -23 * size      # the tolerances of test_gpu_prompt.py
     assert (np.abs(host(lse) - l) <= e + 2.0 ** -20 * (1 + np.abs(l))).all()
     assert (np.abs(host(out) - o) <= (2.0 ** -8 + 2.5 * e + 2.0 ** -19)[..., None] * spread + 2.0 ** -8 * np.abs(o) + 1e-30).all()
+
+
+@pytest.mark.parametrize("flags", ["simt", "tc"])
+@pytest.mark.parametrize("cu_q,cu_k,rows,most_q,bad", [
+    ([0, 5], [0, 9], 5, 0, True),                # no room for a query, and five of them
+    ([0, 5], [0, 9], 0, 5, True),                # no rows at all
+    ([0, 5, 5], [0, 9, 30], 5, 5, True),         # a sequence without queries whose keys end outside
+    ([5, 0, 5], [0, 9, 9], 5, 5, True),          # ends that fall
+    ([0, 5, 5], [0, 9, 9], 5, 5, False), ([0, 0], [0, 0], 0, 0, False), ([2, 2, 2], [1, 1, 9], 5, 5, False),
+])
+def test_debug_checks_see_sequences_that_no_row_belongs_to(cu_q, cu_k, rows, most_q, bad, flags):
+    import torch
+    import speculative_decode_mla_gb300 as lib
+    p = problem(5, 9)
+    p["q"] = p["q"][:rows]
+    status = torch.full((1,), 77, dtype=torch.int32, device="cuda")
+    call = lambda: lib.prompt_attn(**p, cu_q=ints(cu_q), cu_k=ints(cu_k), max_q_len=most_q, max_k_len=9, dev_status=status,
+                                   flags=lib.MLA_FLAG_DEBUG_CHECKS | (lib.MLA_FLAG_SIMT if flags == "simt" else 0))
+    if bad:
+        with pytest.raises(lib.MLAError):
+            call()
+    else:
+        call()
+    assert int(status) == (lib.CHECK_BAD_LENGTH if bad else 0)
