@@ -537,16 +537,27 @@ def verify_kv4(q, pool, slot_table, seq_lens, tree_parent, *, max_seq_len: int, 
 
 @functools.lru_cache(maxsize=1)
 def _empty_call():
+    """(torch's own call for compiled graphs that makes an uninitialised CUDA tensor; the questions that all have to be answered with
+    0 before it may be used), or None where it is gone or not as it was known: a private call, so it is tried out."""
     import torch
-    return getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+    try:
+        c = torch._C
+        # (it passes dispatch and function modes by, and the filling of uninitialised memory in torch's deterministic mode)
+        asks = c._len_torch_dispatch_stack, c._len_torch_function_stack, c._get_deterministic_algorithms
+        call = c._dynamo.guards._empty_strided_cuda
+        t = call((2, 3), (3, 1), torch.bfloat16)
+        known = t.is_cuda and t.shape == (2, 3) and t.stride() == (3, 1) and t.dtype is torch.bfloat16 and all(int(f()) >= 0 for f in asks)
+    except Exception:
+        return None
+    return (call, *asks) if known else None
 
 
 def _empty(shape, strides, dtype, like):
     """An uninitialised tensor on the current device, which is like's. After a launch torch.empty and its methods take 4 to 6 us on
-    the host of a GB300 (they are small and cold then); torch's own call for compiled graphs takes 1.6, where there is one."""
-    call = _empty_call()
-    if call is not None:
-        return call(shape, strides, dtype)
+    the host of a GB300 (they are small and cold then); torch's own call for compiled graphs takes 1.6, where it can be used."""
+    short = _empty_call()
+    if short is not None and not short[1]() and not short[2]() and not short[3]():
+        return short[0](shape, strides, dtype)
     import torch
     return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
 
