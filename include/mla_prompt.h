@@ -87,7 +87,7 @@ int mla_rope_append(const mla_rope_desc *desc, const void *rows, const void *wei
 
 /* Shapes of one mla_prompt_attn call. The launch is a pure function of this struct and of the SM count. */
 typedef struct mla_prompt_desc {
-  int32_t num_seqs;        /* B >= 1 */
+  int32_t num_seqs;        /* B, 1 .. 2^30 */
   int32_t num_heads;       /* H >= 1, query heads */
   int32_t num_kv_heads;    /* >= 1, divides H: query head h reads key head h / (H / num_kv_heads) */
   int32_t max_q_len;       /* host-known upper bound of a sequence's queries, >= 0 */

@@ -29,7 +29,7 @@ int check_prompt(const mla_prompt_desc* d) {
   if (!d || d->num_seqs < 1 || d->num_heads < 1 || d->num_kv_heads < 1 || d->num_heads % d->num_kv_heads != 0)
     return MLA_ERR_INVALID_ARGUMENT;
   if (d->max_q_len < 0 || d->max_k_len < 0 || d->num_q < 0 || d->num_k < 0) return MLA_ERR_INVALID_ARGUMENT;
-  if (d->num_q > kMaxRows || d->num_k > kMaxRows || d->num_q * d->num_heads > 0x7fffff00ll) return MLA_ERR_UNSUPPORTED;
+  if (d->num_seqs > kMaxRows || d->num_q > kMaxRows || d->num_k > kMaxRows || d->num_q * d->num_heads > 0x7fffff00ll) return MLA_ERR_UNSUPPORTED;
   if (d->causal != 0 && d->causal != 1) return MLA_ERR_INVALID_ARGUMENT;
   if (d->out_dtype != MLA_DTYPE_BF16 && d->out_dtype != MLA_DTYPE_F32) return MLA_ERR_INVALID_ARGUMENT;
   if (d->flags & ~(MLA_FLAG_DEBUG_CHECKS | MLA_FLAG_SIMT)) return MLA_ERR_INVALID_ARGUMENT;

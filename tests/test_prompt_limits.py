@@ -20,3 +20,10 @@ def test_scales(lib, scale, want):
                      q_token_stride=384, q_head_stride=192, k_token_stride=256, k_head_stride=128, k_rope_token_stride=64, v_token_stride=256,
                      v_head_stride=128)
     assert lib.mla_prompt_plan(ctypes.byref(d), 152, ctypes.byref(m.PromptPlan())) == want
+
+
+@pytest.mark.parametrize("seqs,want", [(1 << 30, 0), ((1 << 30) + 1, -2), (2 ** 31 - 1, -2)])
+def test_numbers_of_sequences(lib, seqs, want):
+    """The kernels count sequences in 32 bits, in steps of up to 1024 behind the last."""
+    d = m.PromptDesc(num_seqs=seqs, num_heads=1, num_kv_heads=1, max_q_len=1, max_k_len=1, causal=1, softmax_scale=1.0, num_q=1, num_k=1)
+    assert lib.mla_prompt_plan(ctypes.byref(d), 152, ctypes.byref(m.PromptPlan())) == want
