@@ -719,9 +719,11 @@ def prompt_attn(q, k_nope, k_rope, v, cu_q, cu_k=None, *, max_q_len: int, max_k_
     out_type = bf16 if out_dtype == MLA_DTYPE_BF16 else torch.float32
     raw, here = _on(dev, stream)
     with here:
-        # (the cache compares values: a tensor would be found again by its identity, whatever it holds now)
+        # (the cache compares values: a tensor would be found again by its identity, whatever it holds now. A bound may be
+        # past the struct's 32 bits, and a negative one has to stay negative there.)
         desc, need = _prompt_desc(
-            dev, ends - 1, heads, hk, int(max_q_len), int(most_k if max_k_len is None else max_k_len), int(bool(causal)), int(out_dtype),
+            dev, ends - 1, heads, hk, max(-1, min(int(max_q_len), nq)), max(-1, min(int(most_k if max_k_len is None else max_k_len), nk)),
+            int(bool(causal)), int(out_dtype),
             int(DEFAULT_FLAGS if flags is None else flags), int(num_ctas), float(softmax_scale), nq, nk, *q.stride()[:2],
             *k_nope.stride()[:2], k_rope.stride(0), *v.stride()[:2])
         if out is None:

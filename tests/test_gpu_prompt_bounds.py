@@ -90,3 +90,18 @@ def test_debug_checks_see_sequences_that_no_row_belongs_to(cu_q, cu_k, rows, mos
     else:
         call()
     assert int(status) == (lib.CHECK_BAD_LENGTH if bad else 0)
+
+
+@pytest.mark.parametrize("bound", [2 ** 31, 2 ** 32, 2 ** 32 + 7, 2 ** 63 - 1])
+def test_bounds_past_32_bits(bound):
+    """An upper bound may be any number; no sequence has more rows than its tensor."""
+    import torch
+    import speculative_decode_mla_gb300 as lib
+    p = dict(problem(60, 300), cu_q=ints([0, 40, 60]), cu_k=ints([0, 200, 300]))
+    want = lib.prompt_attn(**p, max_q_len=60, max_k_len=300)
+    got = lib.prompt_attn(**p, max_q_len=bound, max_k_len=bound)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(lib.MLAError):
+        lib.prompt_attn(**p, max_q_len=-1, max_k_len=bound)
+    with pytest.raises(lib.MLAError):
+        lib.prompt_attn(**p, max_q_len=bound, max_k_len=-2 ** 32 + 300)
