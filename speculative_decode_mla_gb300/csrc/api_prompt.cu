@@ -18,8 +18,19 @@ namespace mla {
 namespace {
 
 constexpr int64_t kMaxRows = 1ll << 30;
-constexpr int64_t kGroupBytes = 48ll << 20;  // keys and values of the heads that run at a time, in L2
-constexpr int64_t kSharedUnits = 4;          // calls with fewer units than so many times the SMs share their tiles evenly
+// Keys and values of the heads that run at a time, to stay in L2. With 1, 12, 24, 48, 96 MB and without groups, us: 8192 tokens of 64 heads 904,
+// 908, 892, 890, 875, 918; 16,384 of 64 heads 3371, 3420, 3396, 3410, 3404, 3651; 24 prompts of 61 to 2048 tokens of 64 heads 371, 371, 368,
+// 368, 366, 385, of 16 heads 118, 118, 115, 110, 120, 99 (their keys and values fit L2 whole).
+constexpr int64_t kGroupBytes = 48ll << 20;
+// Calls with fewer units than so many times the SMs share their tiles evenly, if there are more than kLeastShare tiles of keys. Whole units / shared,
+// us, at so many units an SM:
+//   4096 tokens, causal       0.5: 58 / 38   1.05: 62 / 56    1.7: 80 / 76     2.0: 87 / 89     3.4: 145 / 139   4.2: 163 / 168   6.7: 256 / 267
+//   4096 tokens, not causal   0.5: 58 / 51   1.05: 113 / 84   1.7: 118 / 125   2.5: 179 / 180   3.4: 236 / 236   4.2: 299 / 308   6.7: 429 / 490
+//   512 after 16 Ki           0.2: 222 / 76  0.8: 236 / 260   1.7: 471 / 497   3.4: 948 / 979
+//   single tokens, 2 Ki       0.8: 31 / 27   1.6: 50 / 39     3.2: 68 / 61     6.7: 121 / 122
+//   1024 tokens, causal       0.6: 22 / 29   1.7: 34 / 44     3.4: 56 / 64     5.3: 83 / 90
+// So 4 is the limit of calls of one lane (single tokens); those of two lanes would gain by one between 1 and 2, and those of few tiles a unit by none.
+constexpr int64_t kSharedUnits = 4;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }

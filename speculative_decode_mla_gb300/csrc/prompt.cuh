@@ -12,7 +12,10 @@ constexpr int kHeadV = 128;                 // dims of a value
 constexpr int kPromptTile = 128;            // keys to a tile, and query rows to an MMA
 constexpr int kMaxPromptCtas = 1024;
 constexpr int kMaxUnitRows = 2 * kPromptTile;
-// What starting and ending a run of tiles costs, in tiles, and the least that a CTA takes in shared calls.
+// What starting and ending a run of tiles costs, in tiles, and the least that a CTA takes in shared calls. Costs of 0, 1, 2, 3, 4, us: 16 heads
+// of 4096 tokens 114, 88, 76, 79, 79; 61 single tokens 63.3, 59.5, 59.4, 59.4, 60.1; 17 tokens after 16 Ki 94.9, 93.8, 97.1, 94.5, 93.7; 16 heads of 512
+// tokens after 16 Ki 77.9, 76.6, 75.5, 76.3, 75.6. Leasts of 2, 3, 4, 6, 8: 8 heads of 1024 tokens 22.5, 24.6, 25.7, 27.9, 19.9, no other of these
+// calls by more than 1%.
 constexpr int kUnitCost = 2, kLeastShare = 4;
 
 // A unit whose last part CTA number c computed, with the first one's CTA: parts first .. c, to be merged.

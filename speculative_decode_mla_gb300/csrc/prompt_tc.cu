@@ -28,10 +28,10 @@
 // (on the diagonal, behind the sequence's end) are looked through first: rows behind the end become 0, and
 // infinities and NaN become 0 and are added to the rows that do see them when O is written, so that they reach no other row.
 //
-// Bound by the tensor cores in long prompts: 8192 tokens of 64 heads 0.91 ms, 1.5 PFLOP/s, 80% of a large library product's rate (a tile
+// Bound by the tensor cores in long prompts: 8192 tokens of 64 heads 0.88 to 0.94 ms, 1.5 PFLOP/s, 80% of a large library product's rate (a tile
 // and both lanes take 3014 cycles, the MMAs 2560; the rest are beginnings and ends of units). By memory where few queries meet many keys: 17
-// tokens after 16 Ki, 64 heads, 94 to 97 us, 5.6 TB/s. By beginnings and ends of units in batches of short prompts: 24 of 61 to 2048
-// tokens, 16 heads, 109 us, 0.75 PFLOP/s.
+// tokens after 16 Ki, 64 heads, 95 to 98 us, 5.6 TB/s. By beginnings and ends of units in batches of short prompts: 24 of 61 to 2048
+// tokens, 16 heads, 110 us, 0.74 PFLOP/s. The kernel of two lanes spills 92 bytes a thread, that of one none.
 //
 // Every wait is bounded (about 2 s, and more for many keys). When one runs out its CTA stops issuing work, drains what is in flight, reports MLA_CHECK_TIMEOUT,
 // gives a NaN lse to the rows of its last two units and of those that it had claimed, or had as its share, and not begun, and exits; a
@@ -932,6 +932,8 @@ __global__ void __launch_bounds__(Layout<ONE>::threads, 1)
             v.x = ex2(v.x);
             v.y = ex2(v.y);
             sum[k & 1] = half == 0 && k < 2 ? v : add2(sum[k & 1], v);
+            // (bf16 as the values are, which an MMA's two operands have to share: 2^-8 of a weight at most. fp16 weights would take values
+            // in fp16, which has not their range. The sum takes them unrounded, so that the roundings do not add up in it.)
             w[k] = pack_bf16(v.x, v.y);
           }
           TMEM_ST32(tS + 32 * half, w);

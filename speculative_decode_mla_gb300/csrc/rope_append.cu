@@ -262,7 +262,8 @@ __device__ __forceinline__ void do_heads(const RopeArgs& a, uint32_t unit) {
   }
 }
 
-// Blocks on an SM and heads in flight: enough bytes under way, without spilled registers. 16,384 tokens, 64 heads of 192 dims,
+// Blocks on an SM and heads in flight: enough bytes under way, with no more than a few registers spilled (40 bytes with norms of 192 dims, 8 with norms
+// and halves of 256, none elsewhere). 16,384 tokens, 64 heads of 192 dims,
 // adjacent pairs, norms, us: one head a group and 4, 5, 6 blocks 153, 143, 143; two and 4, 5, 6 blocks 137, 203, 252 (spills). Pairs half a
 // head apart take more registers: 2111 tokens of 5 heads 5.5 with one head a group, 6.8 with two. Rows alone, 65,536 into the
 // 4-bit pool and read back: 60.5 with 4 blocks, 54.7 with 6, 51.2 with 8.
