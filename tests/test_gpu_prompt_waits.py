@@ -79,7 +79,7 @@ def run(script, *args):
     return r.stdout
 
 
-@pytest.mark.parametrize("cycles", [100000, 3000, 1])
+@pytest.mark.parametrize("cycles", [300000, 3000, 1])
 def test_rows_are_right_or_marked(link, cycles):
     out = run(CALLS, link(WAIT_CYCLES=f"{cycles}ll", WAIT_CYCLES_A_TILE=0))
     assert int(out.split()[-1]) > 0       # (some waits did run out)
@@ -87,4 +87,4 @@ def test_rows_are_right_or_marked(link, cycles):
 
 def test_a_role_without_work_waits_for_a_long_unit(link):
     """The limit grows with the keys: in the calls above lanes without rows wait 400,000 cycles and more for the end of a unit of 313 tiles."""
-    assert int(run(CALLS, link(WAIT_CYCLES="100000ll", WAIT_CYCLES_A_TILE=32768)).split()[-1]) == 0
+    assert int(run(CALLS, link(WAIT_CYCLES="300000ll", WAIT_CYCLES_A_TILE=32768)).split()[-1]) == 0
